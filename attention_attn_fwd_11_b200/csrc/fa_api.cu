@@ -323,6 +323,58 @@ fa_status check_tail(const fa_mla_tail_params *p) {
     return FA_OK;
 }
 
+// ------------------------------------------------- rotary, cache append --
+
+// The rotation of a call: frequencies to 64-bit fractions of a turn.
+fa_status make_rope_map(const char *who, const double *inv_freq, int rot, int offset, int d, int interleaved,
+                        int inverse, float mscale, fa::RopeMap *m) {
+    if (rot <= 0 || rot % 16 != 0 || rot > fa::kMaxRot || offset < 0 || offset % 16 != 0 || offset > d - rot)
+        return fail(FA_ERR_UNSUPPORTED,
+                    "%s: rot_dim and rot_offset must be multiples of 16, rot_dim in (0, %d], rot_offset + rot_dim <= d "
+                    "(got %d, %d)",
+                    who, fa::kMaxRot, rot, offset);
+    if (!isfinite(mscale)) return fail(FA_ERR_INVALID_ARG, "%s: mscale must be finite", who);
+    for (int i = 0; i < rot / 2; ++i) {
+        if (!isfinite(inv_freq[i])) return fail(FA_ERR_INVALID_ARG, "%s: inv_freq[%d] is not finite", who, i);
+        // The fraction is below 1 and has at most 64 significant bits, so the scaled value fits.
+        long double x = (long double)inv_freq[i] / 6.283185307179586476925286766559L;
+        x -= floorl(x);
+        m->turns[i] = x < 1.0L ? (uint64_t)ldexpl(x, 64) : 0;
+    }
+    m->rot = rot;
+    m->offset = offset;
+    m->interleaved = interleaved != 0;
+    m->inverse = inverse != 0;
+    m->mscale = mscale;
+    return FA_OK;
+}
+
+// A tensor [B, H, S, .] of a rotary call: pointers and strides in units of
+// 16 bytes (`unit` elements).  Dimensions of extent 1 may have any stride.
+fa_status check_rows(const char *who, const char *name, const void *src, int64_t sb, int64_t sh, int64_t ss, int B,
+                     int H, int S, int unit) {
+    if (!src) return fail(FA_ERR_INVALID_ARG, "%s: %s is NULL", who, name);
+    if (!aligned16(src)) return fail(FA_ERR_INVALID_ARG, "%s: %s must be 16-byte aligned", who, name);
+    if ((B > 1 && sb % unit) || (H > 1 && sh % unit) || (S > 1 && ss % unit))
+        return fail(FA_ERR_INVALID_ARG, "%s: %s strides must be multiples of %d elements", who, name, unit);
+    return FA_OK;
+}
+
+fa_status rope_tensor(const char *who, const char *name, const void *src, void *dst, int64_t sb, int64_t sh,
+                      int64_t ss, int64_t ob, int64_t oh, int64_t os, int B, int H, int S, int d, int unit,
+                      fa::RopeTensor *t) {
+    fa_status st = check_rows(who, name, src, sb, sh, ss, B, H, S, unit);
+    if (st == FA_OK) st = check_rows(who, name, dst, ob, oh, os, B, H, S, unit);
+    if (st != FA_OK) return st;
+    if ((B > 1 && ob == 0) || (H > 1 && oh == 0) || (S > 1 && os > -d && os < d))
+        return fail(FA_ERR_INVALID_ARG, "%s: the rows of %s's output overlap", who, name);
+    const bool same = (B == 1 || sb == ob) && (H == 1 || sh == oh) && (S == 1 || ss == os);
+    if (src == dst && !same)
+        return fail(FA_ERR_INVALID_ARG, "%s: %s turned in place needs equal strides", who, name);
+    *t = fa::RopeTensor{src, dst, H, sb, sh, ss, ob, oh, os, src == dst};
+    return FA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -824,16 +876,129 @@ fa_status fa_kv_dequant_n(const fa_kv_dequant_params *p, int n, void *stream) {
 
 fa_status fa_kv_dequant(const fa_kv_dequant_params *p, void *stream) { return fa_kv_dequant_n(p, 1, stream); }
 
+fa_status fa_rope(const fa_rope_params *p, void *stream) {
+    const char *who = "fa_rope";
+    if (!p) return fail(FA_ERR_INVALID_ARG, "fa_rope: params is NULL");
+    if (p->B < 0 || p->S < 0 || p->Hq <= 0 || p->Hk < 0 || p->d <= 0)
+        return fail(FA_ERR_INVALID_ARG, "fa_rope: need B, S, Hk >= 0 and Hq, d > 0");
+    if (p->d % 16 != 0 || p->d > 1024)
+        return fail(FA_ERR_UNSUPPORTED, "fa_rope: d must be a multiple of 16 up to 1024 (got %d)", p->d);
+    if ((int64_t)p->B * p->S >= (int64_t(1) << 31) || (int64_t)p->Hq + p->Hk > 65535)
+        return fail(FA_ERR_INVALID_ARG, "fa_rope: B * S must be < 2^31 and Hq + Hk <= 65535");
+    if (p->dtype != FA_F32 && p->dtype != FA_BF16) return fail(FA_ERR_INVALID_ARG, "fa_rope: dtype");
+    if (!p->inv_freq) return fail(FA_ERR_INVALID_ARG, "fa_rope: inv_freq is NULL");
+    if ((uintptr_t)p->pos & 3u) return fail(FA_ERR_INVALID_ARG, "fa_rope: pos must be 4-byte aligned");
+    if ((p->k || p->k_out) && p->Hk == 0) return fail(FA_ERR_INVALID_ARG, "fa_rope: k needs Hk > 0");
+    fa::RopeLaunch L;
+    memset(&L, 0, sizeof L);
+    fa_status st = make_rope_map(who, p->inv_freq, p->rot_dim, p->rot_offset, p->d, p->interleaved, p->inverse,
+                                 p->mscale, &L.map);
+    if (st != FA_OK) return st;
+    if (p->B == 0 || p->S == 0) return FA_OK;
+    const int unit = p->dtype == FA_F32 ? 4 : 8;
+    st = rope_tensor(who, "q", p->q, p->q_out, p->q_sb, p->q_sh, p->q_ss, p->qo_sb, p->qo_sh, p->qo_ss, p->B, p->Hq,
+                     p->S, p->d, unit, &L.x[0]);
+    if (st == FA_OK && p->Hk > 0)
+        st = rope_tensor(who, "k", p->k, p->k_out, p->k_sb, p->k_sh, p->k_ss, p->ko_sb, p->ko_sh, p->ko_ss, p->B,
+                         p->Hk, p->S, p->d, unit, &L.x[1]);
+    if (st != FA_OK) return st;
+    L.B = p->B;
+    L.S = p->S;
+    L.d = p->d;
+    L.pos = p->pos;
+    L.pos_sb = p->pos_sb;
+    L.pos0 = p->pos0;
+    int sms = 0;
+    cudaError_t e = num_sms(&sms);
+    if (e == cudaSuccess) e = fa::launch_rope(L, p->dtype == FA_F32, sms, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "fa_rope: launch");
+    return FA_OK;
+}
+
+fa_status fa_kv_append(const fa_kv_append_params *p, void *stream) {
+    const char *who = "fa_kv_append";
+    if (!p) return fail(FA_ERR_INVALID_ARG, "fa_kv_append: params is NULL");
+    if (p->B < 0 || p->Sq < 0 || p->Hkv <= 0 || p->dk <= 0 || p->dv <= 0 || p->num_blocks <= 0 ||
+        p->max_blocks_per_seq <= 0)
+        return fail(FA_ERR_INVALID_ARG,
+                    "fa_kv_append: need B, Sq >= 0 and Hkv, dk, dv, num_blocks, max_blocks_per_seq > 0");
+    if (p->block_size != 64) return fail(FA_ERR_UNSUPPORTED, "fa_kv_append: block_size must be 64 (got %d)", p->block_size);
+    const bool quant = p->kv_type != FA_KV_BF16;
+    if (quant && p->kv_type != FA_KV_Q8_0 && p->kv_type != FA_KV_Q4_0 && p->kv_type != FA_KV_FP8_E4M3)
+        return fail(FA_ERR_UNSUPPORTED, "fa_kv_append: kv_type %d", p->kv_type);
+    if (p->dk % 16 != 0 || p->dv % 16 != 0 || p->dk > 1024 || p->dv > 1024 ||
+        (quant && (p->dk != 128 || p->dv != 128)))
+        return fail(FA_ERR_UNSUPPORTED,
+                    "fa_kv_append: dk and dv must be multiples of 16 up to 1024, 128 for quantised caches (got %d/%d)",
+                    p->dk, p->dv);
+    if (p->kv_type == FA_KV_FP8_E4M3 && (!finite_pos(p->k_scale) || !finite_pos(p->v_scale)))
+        return fail(FA_ERR_INVALID_ARG, "fa_kv_append: k_scale and v_scale must be finite and > 0");
+    const int Hq = p->q || p->q_out ? p->Hq : 0;
+    if ((p->q || p->q_out) && (p->Hq <= 0 || !p->inv_freq))
+        return fail(FA_ERR_INVALID_ARG, "fa_kv_append: q needs Hq > 0 and inv_freq");
+    if ((int64_t)p->B * p->Sq >= (int64_t(1) << 31) || (int64_t)Hq + 2 * (int64_t)p->Hkv > 65535)
+        return fail(FA_ERR_INVALID_ARG, "fa_kv_append: B * Sq must be < 2^31 and Hq + 2 Hkv <= 65535");
+    if ((uintptr_t)p->pos & 3u) return fail(FA_ERR_INVALID_ARG, "fa_kv_append: pos must be 4-byte aligned");
+    fa::AppendLaunch L;
+    memset(&L, 0, sizeof L);
+    fa_status st = FA_OK;
+    if (p->inv_freq) {
+        st = make_rope_map(who, p->inv_freq, p->rot_dim, p->rot_offset, p->dk, p->interleaved, 0, p->mscale, &L.map);
+        if (st != FA_OK) return st;
+        if ((p->kv_type == FA_KV_Q8_0 || p->kv_type == FA_KV_Q4_0) &&
+            (p->rot_offset % 32 != 0 || p->rot_dim % (p->interleaved ? 32 : 64) != 0))
+            return fail(FA_ERR_UNSUPPORTED,
+                        "fa_kv_append: q8_0 and q4_0 rows need rot_offset %% 32 == 0 and rot_dim %% 64 == 0 "
+                        "(interleaved: 32)");
+    }
+    if (p->B == 0 || p->Sq == 0) return FA_OK;
+    st = check_rows(who, "k", p->k, p->k_sb, p->k_sh, p->k_ss, p->B, p->Hkv, p->Sq, 8);
+    if (st == FA_OK) st = check_rows(who, "v", p->v, p->v_sb, p->v_sh, p->v_ss, p->B, p->Hkv, p->Sq, 8);
+    if (st == FA_OK && Hq > 0)
+        st = rope_tensor(who, "q", p->q, p->q_out, p->q_sb, p->q_sh, p->q_ss, p->qo_sb, p->qo_sh, p->qo_ss, p->B, Hq,
+                         p->Sq, p->dk, 8, &L.q);
+    if (st != FA_OK) return st;
+    if (!p->k_cache || !p->v_cache || !p->block_table || !p->seq_lens)
+        return fail(FA_ERR_INVALID_ARG, "fa_kv_append: NULL cache, block_table or seq_lens");
+    if (!aligned16(p->k_cache) || !aligned16(p->v_cache))
+        return fail(FA_ERR_INVALID_ARG, "fa_kv_append: the caches must be 16-byte aligned");
+    if (((uintptr_t)p->block_table & 3u) || ((uintptr_t)p->seq_lens & 3u) || ((uintptr_t)p->q_lens & 3u))
+        return fail(FA_ERR_INVALID_ARG, "fa_kv_append: block_table, seq_lens and q_lens must be 4-byte aligned");
+    L.k = fa::RopeTensor{p->k, p->k_cache, p->Hkv, p->k_sb, p->k_sh, p->k_ss, 0, 0, 0, 0};
+    L.v = fa::RopeTensor{p->v, p->v_cache, p->Hkv, p->v_sb, p->v_sh, p->v_ss, 0, 0, 0, 0};
+    L.block_table = p->block_table;
+    L.seq_lens = p->seq_lens;
+    L.q_lens = p->q_lens;
+    L.max_blocks = p->max_blocks_per_seq;
+    L.num_blocks = p->num_blocks;
+    L.B = p->B;
+    L.Hkv = p->Hkv;
+    L.Sq = p->Sq;
+    L.dk = p->dk;
+    L.dv = p->dv;
+    L.pos = p->pos;
+    L.pos_sb = p->pos_sb;
+    L.kv_type = p->kv_type;
+    L.k_scale = p->k_scale;
+    L.v_scale = p->v_scale;
+    int sms = 0;
+    cudaError_t e = num_sms(&sms);
+    if (e == cudaSuccess) e = fa::launch_kv_append(L, sms, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "fa_kv_append: launch");
+    return FA_OK;
+}
+
 fa_status fa_device_error(int clear, int *code) {
     if (!code) return fail(FA_ERR_INVALID_ARG, "fa_device_error: code is NULL");
-    int c1 = 0, c2 = 0, c3 = 0, c4 = 0, c5 = 0;
+    int c1 = 0, c2 = 0, c3 = 0, c4 = 0, c5 = 0, c6 = 0;
     cudaError_t e = fa::prefill_device_error(clear, &c1);
     if (e == cudaSuccess) e = fa::tail_device_error(clear, &c5);
     if (e == cudaSuccess) e = fa::prefill2_device_error(clear, &c4);
     if (e == cudaSuccess) e = fa::decode_device_error(clear, &c2);
     if (e == cudaSuccess) e = fa::gather_device_error(clear, &c3);
+    if (e == cudaSuccess) e = fa::append_device_error(clear, &c6);
     if (e != cudaSuccess) return cuda_fail(e, "fa_device_error");
-    *code = c1 ? c1 : (c4 ? c4 : (c2 ? c2 : (c3 ? c3 : c5)));
+    *code = c1 ? c1 : (c4 ? c4 : (c2 ? c2 : (c3 ? c3 : (c5 ? c5 : c6))));
     return FA_OK;
 }
 

@@ -147,4 +147,46 @@ struct KvDequantLaunch {
 constexpr int kMaxDequantSegs = 4;  // tensors one launch converts (all of one type)
 cudaError_t launch_kv_dequant(const KvDequantLaunch *L, int n, int num_sms, cudaStream_t stream);
 
+// ---- rotary positions and the paged cache append (rope.cu) -----------------
+constexpr int kMaxRot = 256;  // rotated columns of a row
+struct RopeMap {
+    uint64_t turns[kMaxRot / 2];  // of each pair: turns per position, as a 64-bit fraction
+    int rot, offset;              // rotated columns [offset, offset + rot); rot 0: none
+    int interleaved, inverse;
+    float mscale;
+};
+struct RopeTensor {  // [B, H, S, d] with element strides; H == 0: absent
+    const void *src;
+    void *dst;
+    int H;
+    int64_t sb, sh, ss, ob, oh, os;
+    int in_place;
+};
+struct RopeLaunch {
+    RopeMap map;
+    RopeTensor x[2];
+    int B, S, d;
+    const int32_t *pos;  // [B, S] at a pitch of pos_sb (0 broadcasts), or NULL: pos0 + s
+    int64_t pos_sb;
+    int pos0;
+    int items, heads;  // set by launch_rope
+};
+cudaError_t launch_rope(RopeLaunch L, bool f32, int num_sms, cudaStream_t stream);
+
+struct AppendLaunch {
+    RopeMap map;
+    RopeTensor q;     // optional (H == 0: absent)
+    RopeTensor k, v;  // src and its strides; dst: the cache (H and the other fields unused)
+    const int32_t *block_table, *seq_lens, *q_lens;
+    int max_blocks, num_blocks;
+    int B, Hkv, Sq, dk, dv;
+    const int32_t *pos;  // NULL: the row's place in its sequence
+    int64_t pos_sb;
+    int kv_type;  // 0: bf16; 8: q8_0, 4: q4_0, 2: fp8 e4m3
+    float k_scale, v_scale;
+    int items, heads, q_groups, kv_groups;  // set by launch_kv_append
+};
+cudaError_t launch_kv_append(AppendLaunch L, int num_sms, cudaStream_t stream);
+cudaError_t append_device_error(int clear, int *code);
+
 }  // namespace fa

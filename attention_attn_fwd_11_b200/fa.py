@@ -74,6 +74,26 @@ class KvDequantParams(ctypes.Structure):
                 ("dst", _vp), ("dst_row_stride", _i64), ("scale", ctypes.c_float)]
 
 
+class RopeParams(ctypes.Structure):
+    _fields_ = [("q", _vp), ("q_out", _vp), ("q_sb", _i64), ("q_sh", _i64), ("q_ss", _i64), ("qo_sb", _i64),
+                ("qo_sh", _i64), ("qo_ss", _i64), ("k", _vp), ("k_out", _vp), ("k_sb", _i64), ("k_sh", _i64),
+                ("k_ss", _i64), ("ko_sb", _i64), ("ko_sh", _i64), ("ko_ss", _i64), ("B", _i32), ("Hq", _i32),
+                ("Hk", _i32), ("S", _i32), ("d", _i32), ("dtype", _i32), ("pos", _vp), ("pos_sb", _i64),
+                ("pos0", _i32), ("inv_freq", _vp), ("rot_dim", _i32), ("rot_offset", _i32), ("interleaved", _i32),
+                ("inverse", _i32), ("mscale", ctypes.c_float)]
+
+
+class KvAppendParams(ctypes.Structure):
+    _fields_ = [("k", _vp), ("v", _vp), ("k_sb", _i64), ("k_sh", _i64), ("k_ss", _i64), ("v_sb", _i64),
+                ("v_sh", _i64), ("v_ss", _i64), ("k_cache", _vp), ("v_cache", _vp), ("block_table", _vp),
+                ("seq_lens", _vp), ("q_lens", _vp), ("max_blocks_per_seq", _i32), ("B", _i32), ("Hkv", _i32),
+                ("Sq", _i32), ("dk", _i32), ("dv", _i32), ("block_size", _i32), ("num_blocks", _i32),
+                ("kv_type", _i32), ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float), ("inv_freq", _vp),
+                ("rot_dim", _i32), ("rot_offset", _i32), ("interleaved", _i32), ("mscale", ctypes.c_float),
+                ("pos", _vp), ("pos_sb", _i64), ("q", _vp), ("q_out", _vp), ("Hq", _i32), ("q_sb", _i64),
+                ("q_sh", _i64), ("q_ss", _i64), ("qo_sb", _i64), ("qo_sh", _i64), ("qo_ss", _i64)]
+
+
 FA_KV_Q8_0, FA_KV_Q4_0, FA_KV_FP8_E4M3 = 8, 4, 2
 KV_QUANT = {"q8_0": (FA_KV_Q8_0, 34), "q4_0": (FA_KV_Q4_0, 18),
             "fp8_e4m3": (FA_KV_FP8_E4M3, 32)}  # type code, bytes per 32 values
@@ -108,6 +128,10 @@ def load():
         lib.fa_kv_dequant.restype = _i32
         lib.fa_kv_dequant_n.argtypes = [ctypes.POINTER(KvDequantParams), _i32, _vp]
         lib.fa_kv_dequant_n.restype = _i32
+        lib.fa_rope.argtypes = [ctypes.POINTER(RopeParams), _vp]
+        lib.fa_rope.restype = _i32
+        lib.fa_kv_append.argtypes = [ctypes.POINTER(KvAppendParams), _vp]
+        lib.fa_kv_append.restype = _i32
         lib.fa_last_error.argtypes = []
         lib.fa_last_error.restype = ctypes.c_char_p
         lib.fa_device_error.argtypes = [_i32, ctypes.POINTER(_i32)]
@@ -142,6 +166,14 @@ def _need_cuda(*ts):
     for t in ts:
         if t is not None and not t.is_cuda:
             raise ValueError("libfa works on CUDA tensors only (no CPU fallback)")
+
+
+def _need_current_device(*ts):
+    """CUDA tensors of one device, the current one (the library launches there)."""
+    _need_cuda(*ts)
+    for t in ts:
+        if t is not None and t.device.index != torch.cuda.current_device():
+            raise ValueError("every tensor must be on the current CUDA device (see torch.cuda.device)")
 
 
 def _odt(dtype):
@@ -543,3 +575,180 @@ def mla_tail(o_lat, w_abs, w_o, out=None, out_dtype=torch.float32, num_splits=0,
     p = mla_tail_params(o_lat, w_abs, w_o, out, num_splits, workspace)
     _check(load().fa_mla_tail(ctypes.byref(p), _stream(stream)))
     return out
+
+
+# --------------------------------------------------------- rotary positions --
+
+def rope_frequencies(rot_dim, base=10000.0, scaling=None, factor=1.0, original_len=None, beta_fast=32.0,
+                     beta_slow=1.0):
+    """Angular frequencies for rope() and kv_append(): base ** (-2 i / rot_dim)
+    for i < rot_dim / 2, as a float64 CPU tensor, and the factor (mscale) on
+    the rotated columns.  For contexts ``factor`` (>= 1) times as long as the
+    trained ``original_len``, scaling is one of
+      None      none;
+      "linear"  every frequency / factor;
+      "ntk"     a larger base, factor ** (rot_dim / (rot_dim - 2)) times: the
+                slowest pair is slowed by factor, the fastest not at all;
+      "yarn"    by parts: pairs that turn more than beta_fast times over
+                original_len are kept, those below beta_slow turns are slowed
+                by factor, with a ramp over the pair index between, and
+                mscale = 0.1 ln(factor) + 1.
+    Returns (inv_freq, mscale)."""
+    if rot_dim <= 0 or rot_dim % 2:
+        raise ValueError("rot_dim must be positive and even")
+    if not base > 1.0 or not factor >= 1.0:
+        raise ValueError("base must be > 1 and factor >= 1")
+    i = torch.arange(rot_dim // 2, dtype=torch.float64)
+    if scaling == "ntk":
+        if rot_dim == 2:
+            raise ValueError('scaling "ntk" needs rot_dim > 2')
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    inv = base ** (-2.0 * i / rot_dim)
+    if scaling is None or scaling == "ntk":
+        return inv, 1.0
+    if scaling == "linear":
+        return inv / factor, 1.0
+    if scaling != "yarn":
+        raise ValueError('scaling must be None, "linear", "ntk" or "yarn"')
+    if original_len is None or original_len <= 0 or not beta_fast > beta_slow > 0:
+        raise ValueError('scaling "yarn" needs original_len > 0 and beta_fast > beta_slow > 0')
+
+    def pair(turns):  # the (fractional) pair that turns this often over original_len
+        return rot_dim * math.log(original_len / (turns * 2 * math.pi)) / (2 * math.log(base))
+
+    low = max(0, math.floor(pair(beta_fast)))
+    high = min(rot_dim - 1, math.ceil(pair(beta_slow)))
+    ramp = ((i - low) / max(high - low, 1e-3)).clamp(0, 1)
+    return inv / factor * ramp + inv * (1 - ramp), 0.1 * math.log(factor) + 1.0
+
+
+def _check_inv_freq(inv_freq):
+    if inv_freq.dtype != torch.float64 or inv_freq.is_cuda or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be a 1-D contiguous float64 CPU tensor (see rope_frequencies)")
+
+
+def _check_pos(pos, B, S):
+    """Pitch of pos over the batch (0 broadcasts)."""
+    if pos.dtype != torch.int32 or (S > 1 and pos.stride(-1) != 1) or tuple(pos.shape) not in ((S,), (1, S), (B, S)):
+        raise ValueError("pos must be an int32 tensor [S], [1, S] or [B, S] with a contiguous last dim")
+    return pos.stride(0) if pos.dim() == 2 and pos.shape[0] > 1 else 0
+
+
+def _rope_out(x, out):
+    if out is None:
+        return torch.empty(x.shape, device=x.device, dtype=x.dtype)
+    if out.shape != x.shape or out.dtype != x.dtype or out.stride(3) != 1:
+        raise ValueError("an output must have its input's shape and dtype and a contiguous last dim")
+    return out
+
+
+def rope(q, inv_freq, k=None, pos=None, pos0=0, interleaved=False, offset=0, inverse=False, mscale=1.0, out=None,
+         k_out=None, stream=None):
+    """Rotary positions (fa_rope): the pairs of columns [offset, offset + 2
+    len(inv_freq)) of q [B,Hq,S,d] and, if given, k [B,Hk,S,d] turned by their
+    row's position times inv_freq (float64 CPU tensor, see rope_frequencies),
+    one launch for both.  bf16 or fp32, any strides with a contiguous last
+    dim.  pos: int32 CUDA tensor [S], [1,S] or [B,S], or None: row s is at
+    pos0 + s.  inverse=True turns back: the gradient.  out / k_out may be
+    given, also as q / k themselves.  Returns (q turned, k turned or None)."""
+    _need_current_device(q, k, pos, out, k_out)
+    for t in (q, k):
+        if t is not None and (t.dtype not in (torch.bfloat16, torch.float32) or t.dim() != 4 or t.stride(3) != 1 or
+                              t.dtype != q.dtype):
+            raise ValueError("q and k must be 4-D tensors of one dtype, bf16 or fp32, with a contiguous last dim")
+    if k is not None and (k.shape[0], k.shape[2], k.shape[3]) != (q.shape[0], q.shape[2], q.shape[3]):
+        raise ValueError("k must be [B, Hk, S, d] with q's B, S and d")
+    if k is None and k_out is not None:
+        raise ValueError("k_out without k")
+    _check_inv_freq(inv_freq)
+    B, Hq, S, d = q.shape
+    out = _rope_out(q, out)
+    p = RopeParams()
+    p.q, p.q_out = _ptr(q), _ptr(out)
+    p.q_sb, p.q_sh, p.q_ss = q.stride()[:3]
+    p.qo_sb, p.qo_sh, p.qo_ss = out.stride()[:3]
+    p.B, p.Hq, p.S, p.d = B, Hq, S, d
+    if k is not None:
+        k_out = _rope_out(k, k_out)
+        p.k, p.k_out, p.Hk = _ptr(k), _ptr(k_out), k.shape[1]
+        p.k_sb, p.k_sh, p.k_ss = k.stride()[:3]
+        p.ko_sb, p.ko_sh, p.ko_ss = k_out.stride()[:3]
+    p.dtype = _odt(q.dtype)
+    if pos is not None:
+        p.pos_sb = _check_pos(pos, B, S)
+        p.pos = _ptr(pos)
+    p.pos0 = pos0
+    p.inv_freq, p.rot_dim, p.rot_offset = _ptr(inv_freq), 2 * inv_freq.numel(), offset
+    p.interleaved, p.inverse, p.mscale = int(interleaved), int(inverse), mscale
+    _check(load().fa_rope(ctypes.byref(p), _stream(stream)))
+    return out, k_out
+
+
+# ------------------------------------------------------ paged cache append --
+
+def kv_append(k, v, k_cache, v_cache, block_table, seq_lens, q_lens=None, inv_freq=None, mscale=1.0, pos=None,
+              interleaved=False, offset=0, q=None, q_out=None, kv_type=None, k_scale=1.0, v_scale=1.0, stream=None):
+    """New rows into a paged cache (fa_kv_append): k [B,Hkv,Sq,dk] and v
+    [B,Hkv,Sq,dv] (bf16, any strides with a contiguous last dim) go to the
+    last places of their sequences, whose lengths seq_lens [B] INCLUDE them
+    (q_lens [B]: how many of the Sq rows each sequence has).  Caches,
+    block_table and kv_type as in decode_paged().  With inv_freq the columns
+    [offset, offset + 2 len(inv_freq)) of k are turned as by rope() first, at
+    pos (int32 [B,Sq], [1,Sq] or [Sq]) or else the row's place in its
+    sequence; q [B,Hq,Sq,dk], if given, is turned too.  Returns q turned (in
+    q_out, which may be q; rows past q_lens are zeros), or None without q."""
+    _need_current_device(k, v, k_cache, v_cache, block_table, seq_lens, q_lens, q, q_out, pos)
+    for t in (k, v) + ((q,) if q is not None else ()):
+        if t.dtype != torch.bfloat16 or t.dim() != 4 or t.stride(3) != 1:
+            raise ValueError("k, v and q must be 4-D bf16 with a contiguous last dim")
+    if k.shape[:3] != v.shape[:3]:
+        raise ValueError("k and v must have one B, Hkv and Sq")
+    B, Hkv, Sq, dk = k.shape
+    dv = v.shape[3]
+    for c, d in ((k_cache, dk), (v_cache, dv)):
+        if c.dim() != 4 or not c.is_contiguous() or c.shape[1] != Hkv or c.shape[:3] != k_cache.shape[:3]:
+            raise ValueError("the caches must be contiguous [num_blocks, Hkv, block_size, row] with k's Hkv")
+        if c.dtype != k_cache.dtype or c.dtype not in (torch.bfloat16, torch.uint8):
+            raise ValueError("the caches must both be bf16, or both uint8 rows of a quantised type")
+        if c.dtype == torch.bfloat16 and c.shape[3] != d:
+            raise ValueError("the rows of a bf16 cache must be as wide as those of k and v")
+    p = KvAppendParams()
+    if k_cache.dtype == torch.uint8:
+        kv_type, _ = _paged_kv(k, k_cache, kv_type)
+        if any(c.shape[3] != d // 32 * KV_QUANT[kv_type][1] for c, d in ((k_cache, dk), (v_cache, dv))):
+            raise ValueError("the cache rows do not hold k's and v's rows as " + kv_type)
+        p.kv_type, p.k_scale, p.v_scale = KV_QUANT[kv_type][0], k_scale, v_scale
+    elif kv_type is not None:
+        raise ValueError("kv_type is for uint8 caches")
+    for t in (block_table, seq_lens) + ((q_lens,) if q_lens is not None else ()):
+        if t.dtype != torch.int32 or not t.is_contiguous() or t.shape[0] != B or t.dim() != (2 if t is block_table else 1):
+            raise ValueError("block_table [B, max_blocks], seq_lens [B] and q_lens [B] must be contiguous int32")
+    p.k, p.v = _ptr(k), _ptr(v)
+    p.k_sb, p.k_sh, p.k_ss = k.stride()[:3]
+    p.v_sb, p.v_sh, p.v_ss = v.stride()[:3]
+    p.k_cache, p.v_cache = _ptr(k_cache), _ptr(v_cache)
+    p.block_table, p.seq_lens, p.q_lens = _ptr(block_table), _ptr(seq_lens), _ptr(q_lens)
+    p.max_blocks_per_seq = block_table.shape[1]
+    p.B, p.Hkv, p.Sq, p.dk, p.dv = B, Hkv, Sq, dk, dv
+    p.block_size, p.num_blocks = k_cache.shape[2], k_cache.shape[0]
+    p.mscale = mscale
+    if inv_freq is not None:
+        _check_inv_freq(inv_freq)
+        p.inv_freq, p.rot_dim, p.rot_offset = _ptr(inv_freq), 2 * inv_freq.numel(), offset
+        p.interleaved = int(interleaved)
+    if pos is not None:
+        p.pos_sb = _check_pos(pos, B, Sq)
+        p.pos = _ptr(pos)
+    if q is not None:
+        if inv_freq is None:
+            raise ValueError("q without inv_freq: there is nothing to turn it by")
+        if (q.shape[0], q.shape[2], q.shape[3]) != (B, Sq, dk):
+            raise ValueError("q must be [B, Hq, Sq, dk] with k's B, Sq and dk")
+        q_out = _rope_out(q, q_out)
+        p.q, p.q_out, p.Hq = _ptr(q), _ptr(q_out), q.shape[1]
+        p.q_sb, p.q_sh, p.q_ss = q.stride()[:3]
+        p.qo_sb, p.qo_sh, p.qo_ss = q_out.stride()[:3]
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _check(load().fa_kv_append(ctypes.byref(p), _stream(stream)))
+    return q_out

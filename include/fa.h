@@ -423,6 +423,114 @@ fa_status fa_kv_dequant_n(const fa_kv_dequant_params *p, int n, void *stream);
 fa_status fa_decode_gather_workspace_size(const fa_decode_gather_params *p, size_t *bytes);
 fa_status fa_decode_gather(const fa_decode_gather_params *p, void *stream);
 
+/*
+ * fa_rope -- rotary positions: pairs of columns of q and k turned by an angle
+ * that grows with the row's position p, pair i by a_i = p * inv_freq[i]:
+ *   y0 = mscale (x0 cos a_i - x1 sin a_i),  y1 = mscale (x1 cos a_i + x0 sin a_i)
+ * inverse != 0 turns back (-a_i): applied to the gradient of y it gives the
+ * gradient of x.
+ *   q: [B, Hq, S, d] (dtype: FA_BF16 or FA_F32), k: [B, Hk, S, d] or absent
+ *     (k NULL, Hk 0).  q_out, k_out: the same shapes and dtype; each may be
+ *     its input (same strides) and may not overlap it otherwise.  The result
+ *     is computed in fp32 and rounded once.
+ *   Strides (elements) give batch / head / sequence steps, multiples of 8
+ *     for bf16 and 4 for fp32 (an input's may be 0); base pointers 16-byte
+ *     aligned.
+ *   inv_freq: rot_dim / 2 angular frequencies (radians per position) in HOST
+ *     memory, finite, read during the call.  Any scaling for long contexts is
+ *     in them and in mscale (finite).  The angles are exact to 1.5e-9 radians
+ *     at any position.
+ *   Columns [rot_offset, rot_offset + rot_dim) are rotated, the others are
+ *     copied (left alone where the output is the input).  Pair i is columns
+ *     (i, i + rot_dim / 2) of them, or with interleaved != 0 (2i, 2i + 1).
+ *   pos: NULL (row s is at position pos0 + s) or int32, the position of row s
+ *     of batch entry b at b * pos_sb + s (pos_sb 0 broadcasts); may be
+ *     negative.
+ * Requirements: d, rot_dim and rot_offset multiples of 16, d <= 1024,
+ * 0 < rot_dim <= 256, rot_offset + rot_dim <= d; otherwise
+ * FA_ERR_UNSUPPORTED.  B * S < 2^31, Hq + Hk <= 65535.
+ * B == 0 or S == 0 is a no-op.
+ */
+typedef struct {
+    const void *q;
+    void *q_out;
+    int64_t q_sb, q_sh, q_ss, qo_sb, qo_sh, qo_ss;
+    const void *k;
+    void *k_out;
+    int64_t k_sb, k_sh, k_ss, ko_sb, ko_sh, ko_ss;
+    int B, Hq, Hk, S, d;
+    int dtype; /* fa_dtype */
+    const int32_t *pos;
+    int64_t pos_sb;
+    int pos0;
+    const double *inv_freq; /* host */
+    int rot_dim, rot_offset, interleaved, inverse;
+    float mscale;
+} fa_rope_params;
+
+fa_status fa_rope(const fa_rope_params *p, void *stream);
+
+/*
+ * fa_kv_append -- writes the K and V rows of new tokens into the paged cache
+ * that fa_decode_paged and fa_prefill_paged read, K (and, if given, q) turned
+ * as by fa_rope on the way, in one launch.
+ *   k: [B, Hkv, Sq, dk], v: [B, Hkv, Sq, dv] bf16, strides as in fa_rope.
+ *   k_cache, v_cache, block_table, max_blocks_per_seq, num_blocks,
+ *     block_size, seq_lens, q_lens: as in fa_prefill_paged; seq_lens INCLUDES
+ *     the new tokens, and new row i of sequence b (i < n_b = q_lens[b]
+ *     clamped to [0, Sq], or Sq) goes to place seq_lens[b] - n_b + i of its
+ *     sequence.  Rows whose place is negative are not written; every other
+ *     slot of the cache keeps its bytes.
+ *   kv_type: FA_KV_BF16, or the quantised rows of fa_decode_paged (layouts as
+ *     in fa_kv_dequant; the rotated row is quantised from fp32):
+ *       FA_KV_Q8_0: d = the block's largest magnitude / 127, stored as f16;
+ *         code = x / d to the nearest, ties to even, in [-127, 127];
+ *       FA_KV_Q4_0: d = the value of largest magnitude (the first of equals)
+ *         / -8, stored as f16; nibble = 8 + (x / d to the nearest, ties to
+ *         even, in [-8, 7]);
+ *       FA_KV_FP8_E4M3: x / k_scale (or v_scale), limited to +-448, to the
+ *         nearest e4m3, ties to even.
+ *     d is the f16 that is stored; where it is 0 the codes are 0.  |d| is
+ *     limited to 65504; a block with an infinite or NaN value gets d = NaN.
+ *   inv_freq, rot_dim, rot_offset, interleaved, mscale: as in fa_rope;
+ *     inv_freq NULL: nothing is turned (rot_dim is ignored).
+ *   pos: NULL (a row's position is its place in the sequence) or int32, the
+ *     position of new row i of sequence b at b * pos_sb + i.
+ *   q: NULL, or [B, Hq, Sq, dk] bf16, turned like k into q_out (which may be
+ *     q); rows past n_b are written as zeros.  Needs inv_freq.
+ * Supported: block_size == 64; bf16: dk and dv multiples of 16 up to 1024;
+ * quantised: dk == dv == 128, and for FA_KV_Q8_0 and FA_KV_Q4_0 blocks that
+ * the pairs do not straddle: rot_offset a multiple of 32 and rot_dim one of
+ * 64 (interleaved: 32).
+ * A place past the table's end, or a block id outside [0, num_blocks), is
+ * latched as FA_DEVERR_BAD_BLOCK and the row is not written.  No two new rows
+ * may share a slot (a block that two sequences' tables name for new rows).
+ * B == 0 or Sq == 0 is a no-op.
+ */
+typedef struct {
+    const void *k, *v;
+    int64_t k_sb, k_sh, k_ss, v_sb, v_sh, v_ss;
+    void *k_cache, *v_cache;
+    const int32_t *block_table;
+    const int32_t *seq_lens;
+    const int32_t *q_lens;
+    int max_blocks_per_seq;
+    int B, Hkv, Sq, dk, dv, block_size, num_blocks;
+    int kv_type; /* fa_kv_quant */
+    float k_scale, v_scale; /* FA_KV_FP8_E4M3: finite and > 0 */
+    const double *inv_freq; /* host, or NULL */
+    int rot_dim, rot_offset, interleaved;
+    float mscale;
+    const int32_t *pos;
+    int64_t pos_sb;
+    const void *q;
+    void *q_out;
+    int Hq;
+    int64_t q_sb, q_sh, q_ss, qo_sb, qo_sh, qo_ss;
+} fa_kv_append_params;
+
+fa_status fa_kv_append(const fa_kv_append_params *p, void *stream);
+
 /* Message for the last non-OK status returned on this host thread. */
 const char *fa_last_error(void);
 
