@@ -375,6 +375,42 @@ fa_status rope_tensor(const char *who, const char *name, const void *src, void *
     return FA_OK;
 }
 
+// -------------------------------------------------------------- backward --
+
+fa_status check_bwd(const fa_bwd_params *p) {
+    if (!p) return fail(FA_ERR_INVALID_ARG, "fa_bwd: params is NULL");
+    if (p->B < 0 || p->Hq <= 0 || p->Hkv <= 0 || p->Sq < 0 || p->Sk < 0)
+        return fail(FA_ERR_INVALID_ARG, "fa_bwd: need B >= 0, Hq > 0, Hkv > 0, Sq >= 0, Sk >= 0");
+    if (p->Hq % p->Hkv != 0) return fail(FA_ERR_INVALID_ARG, "fa_bwd: Hq (%d) %% Hkv (%d) != 0", p->Hq, p->Hkv);
+    if (!((p->dk == 64 && p->dv == 64) || (p->dk == 128 && p->dv == 128) || (p->dk == 192 && p->dv == 128)))
+        return fail(FA_ERR_UNSUPPORTED, "fa_bwd: supported (dk, dv) = (64, 64), (128, 128), (192, 128); got (%d, %d)",
+                    p->dk, p->dv);
+    if (!finite_pos(p->scale)) return fail(FA_ERR_INVALID_ARG, "fa_bwd: scale must be finite and > 0");
+    if ((p->o_dtype != FA_F32 && p->o_dtype != FA_BF16) || (p->g_dtype != FA_F32 && p->g_dtype != FA_BF16))
+        return fail(FA_ERR_INVALID_ARG, "fa_bwd: o_dtype, g_dtype");
+    if (p->Sq > (1 << 30) || p->Sk > (1 << 30) ||
+        ((int64_t)p->Sq / 64 + 2) * (int64_t)p->B * p->Hq > 0x3fffffffLL ||
+        ((int64_t)p->Sk / 64 + 2) * (int64_t)p->B * p->Hkv > 0x3fffffffLL)
+        return fail(FA_ERR_INVALID_ARG, "fa_bwd: sizes out of range");
+    if (!isfinite(p->max_bias) || p->max_bias < 0.f || !isfinite(p->softcap) || p->softcap < 0.f)
+        return fail(FA_ERR_INVALID_ARG, "fa_bwd: max_bias and softcap must be finite and >= 0");
+    return FA_OK;
+}
+
+size_t bwd_row_bytes(const fa_bwd_params *p) {  // of the row LSE, and of D
+    const size_t n = (size_t)p->B * p->Hq * (size_t)fa::bwd_pitch(p->Sq) * sizeof(float);
+    return (n + 255) & ~size_t(255);
+}
+
+// A gradient's strides: vector stores of 16 bytes, rows that do not overlap.
+fa_status check_grad(const char *name, const void *g, int64_t sb, int64_t sh, int64_t ss, int d, int unit) {
+    if (!g || !aligned16(g)) return fail(FA_ERR_INVALID_ARG, "fa_bwd: %s is NULL or not 16-byte aligned", name);
+    if (sb % unit || sh % unit || ss % unit || ss < d)
+        return fail(FA_ERR_INVALID_ARG, "fa_bwd: %s strides must be multiples of %d elements, rows >= the width", name,
+                    unit);
+    return FA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -988,17 +1024,130 @@ fa_status fa_kv_append(const fa_kv_append_params *p, void *stream) {
     return FA_OK;
 }
 
+fa_status fa_bwd_workspace_size(const fa_bwd_params *p, size_t *bytes) {
+    fa_status st = check_bwd(p);
+    if (st != FA_OK) return st;
+    if (!bytes) return fail(FA_ERR_INVALID_ARG, "fa_bwd_workspace_size: bytes is NULL");
+    *bytes = 2 * bwd_row_bytes(p);
+    return FA_OK;
+}
+
+fa_status fa_bwd(const fa_bwd_params *p, void *stream) {
+    fa_status st = check_bwd(p);
+    if (st != FA_OK) return st;
+    if (p->gsinks && !p->sinks) return fail(FA_ERR_INVALID_ARG, "fa_bwd: gsinks needs sinks");
+    if (((uintptr_t)p->sinks & 3u) || ((uintptr_t)p->gsinks & 3u) || ((uintptr_t)p->lse & 3u) ||
+        ((uintptr_t)p->dlse & 3u))
+        return fail(FA_ERR_INVALID_ARG, "fa_bwd: lse, dlse, sinks and gsinks must be 4-byte aligned");
+    const bool rows = p->B > 0 && p->Sq > 0, keys = p->B > 0 && p->Sk > 0;
+    if (!rows && !keys && !p->gsinks) return FA_OK;
+    if (rows) {
+        if (!p->q || !p->o || !p->dout || !p->lse || !aligned16(p->q) || !aligned16(p->o) || !aligned16(p->dout))
+            return fail(FA_ERR_INVALID_ARG, "fa_bwd: q, o, dout, lse must be given, tensors 16-byte aligned");
+        const int ovec = p->o_dtype == FA_F32 ? 4 : 8;
+        if (p->o_ss % ovec || p->o_sh % ovec || p->o_sb % ovec)
+            return fail(FA_ERR_INVALID_ARG, "fa_bwd: o strides must be multiples of %d elements", ovec);
+    }
+    if (keys && (!p->k || !p->v || !aligned16(p->k) || !aligned16(p->v)))
+        return fail(FA_ERR_INVALID_ARG, "fa_bwd: k and v must be given, 16-byte aligned");
+    const int gvec = p->g_dtype == FA_F32 ? 4 : 8;
+    if (rows) st = check_grad("gq", p->gq, p->gq_sb, p->gq_sh, p->gq_ss, p->dk, gvec);
+    if (st == FA_OK && keys) st = check_grad("gk", p->gk, p->gk_sb, p->gk_sh, p->gk_ss, p->dk, gvec);
+    if (st == FA_OK && keys) st = check_grad("gv", p->gv, p->gv_sb, p->gv_sh, p->gv_ss, p->dv, gvec);
+    if (st != FA_OK) return st;
+    if (p->mask && (((uintptr_t)p->mask & 15u) || p->m_ss % 8 || p->m_sh % 8 || p->m_sb % 8 || p->m_ss < p->Sk ||
+                    p->m_sh < 0 || p->m_sb < 0))
+        return fail(FA_ERR_INVALID_ARG,
+                    "fa_bwd: mask must be 16-byte aligned, its strides multiples of 8 elements, m_ss >= Sk");
+    const size_t each = bwd_row_bytes(p), need = 2 * each;
+    if (need > 0 && (!p->workspace || p->workspace_bytes < need || ((uintptr_t)p->workspace & 255u)))
+        return fail(FA_ERR_WORKSPACE, "fa_bwd: workspace needs %zu bytes, 256-byte aligned", need);
+    if (!get_encoder()) return fail(FA_ERR_CUDA, "fa_bwd: cuTensorMapEncodeTiled is not available");
+    fa::BwdLaunch L;
+    memset(&L, 0, sizeof L);
+    // A side without rows is never loaded; its maps stay empty.
+    const auto both = [&](CUtensorMap *x, CUtensorMap *y, const void *t, int d, int S, int H, int64_t ss, int64_t sh,
+                          int64_t sb, const char *name) {
+        fa_status r = encode_4d(x, t, d, S, H, p->B, ss, sh, sb, 128, name);
+        return r == FA_OK ? encode_4d(y, t, d, S, H, p->B, ss, sh, sb, 64, name) : r;
+    };
+    if (rows) {
+        st = both(&L.tmQx, &L.tmQy, p->q, p->dk, p->Sq, p->Hq, p->q_ss, p->q_sh, p->q_sb, "fa_bwd q");
+        if (st == FA_OK)
+            st = both(&L.tmDOx, &L.tmDOy, p->dout, p->dv, p->Sq, p->Hq, p->do_ss, p->do_sh, p->do_sb, "fa_bwd dout");
+    }
+    if (st == FA_OK && keys) {
+        st = both(&L.tmKx, &L.tmKy, p->k, p->dk, p->Sk, p->Hkv, p->k_ss, p->k_sh, p->k_sb, "fa_bwd k");
+        if (st == FA_OK) st = both(&L.tmVx, &L.tmVy, p->v, p->dv, p->Sk, p->Hkv, p->v_ss, p->v_sh, p->v_sb, "fa_bwd v");
+    }
+    if (st != FA_OK) return st;
+    L.B = p->B;
+    L.Hq = p->Hq;
+    L.Hkv = p->Hkv;
+    L.Sq = p->Sq;
+    L.Sk = p->Sk;
+    L.dk = p->dk;
+    L.dv = p->dv;
+    L.scale = p->scale;
+    L.causal = p->causal ? 1 : 0;
+    L.o = p->o;
+    L.dout = p->dout;
+    L.o_sb = p->o_sb;
+    L.o_sh = p->o_sh;
+    L.o_ss = p->o_ss;
+    L.do_sb = p->do_sb;
+    L.do_sh = p->do_sh;
+    L.do_ss = p->do_ss;
+    L.o_bf16 = p->o_dtype == FA_BF16;
+    L.lse = p->lse;
+    L.dlse = p->dlse;
+    L.gq = p->gq;
+    L.gk = p->gk;
+    L.gv = p->gv;
+    L.gq_sb = p->gq_sb;
+    L.gq_sh = p->gq_sh;
+    L.gq_ss = p->gq_ss;
+    L.gk_sb = p->gk_sb;
+    L.gk_sh = p->gk_sh;
+    L.gk_ss = p->gk_ss;
+    L.gv_sb = p->gv_sb;
+    L.gv_sh = p->gv_sh;
+    L.gv_ss = p->gv_ss;
+    L.g_bf16 = p->g_dtype == FA_BF16;
+    L.mods.mask = static_cast<const __half *>(p->mask);
+    L.mods.m_sb = p->m_sb;
+    L.mods.m_sh = p->m_sh;
+    L.mods.m_ss = p->m_ss;
+    L.mods.softcap = p->softcap;
+    L.mods.sinks = p->sinks;
+    if (p->max_bias > 0.f) {  // ALiBi bases, as read in score_mods.cuh
+        int n2 = 1;
+        while (n2 * 2 <= p->Hq) n2 *= 2;
+        L.mods.n_head_log2 = n2;
+        L.mods.log2_m0 = -p->max_bias / (float)n2;
+        L.mods.log2_m1 = -p->max_bias / 2.f / (float)n2;
+    }
+    L.has_mods = p->mask || p->softcap > 0.f;
+    L.gsinks = p->gsinks;
+    L.lse2 = static_cast<float *>(p->workspace);
+    L.delta = reinterpret_cast<float *>(static_cast<char *>(p->workspace) + each);
+    cudaError_t e = fa::launch_bwd(L, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "fa_bwd: launch");
+    return FA_OK;
+}
+
 fa_status fa_device_error(int clear, int *code) {
     if (!code) return fail(FA_ERR_INVALID_ARG, "fa_device_error: code is NULL");
-    int c1 = 0, c2 = 0, c3 = 0, c4 = 0, c5 = 0, c6 = 0;
+    int c1 = 0, c2 = 0, c3 = 0, c4 = 0, c5 = 0, c6 = 0, c7 = 0;
     cudaError_t e = fa::prefill_device_error(clear, &c1);
     if (e == cudaSuccess) e = fa::tail_device_error(clear, &c5);
     if (e == cudaSuccess) e = fa::prefill2_device_error(clear, &c4);
     if (e == cudaSuccess) e = fa::decode_device_error(clear, &c2);
     if (e == cudaSuccess) e = fa::gather_device_error(clear, &c3);
     if (e == cudaSuccess) e = fa::append_device_error(clear, &c6);
+    if (e == cudaSuccess) e = fa::bwd_device_error(clear, &c7);
     if (e != cudaSuccess) return cuda_fail(e, "fa_device_error");
-    *code = c1 ? c1 : (c4 ? c4 : (c2 ? c2 : (c3 ? c3 : (c5 ? c5 : c6))));
+    *code = c1 ? c1 : (c4 ? c4 : (c2 ? c2 : (c3 ? c3 : (c5 ? c5 : (c6 ? c6 : c7)))));
     return FA_OK;
 }
 

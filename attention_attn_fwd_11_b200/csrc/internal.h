@@ -189,4 +189,29 @@ struct AppendLaunch {
 cudaError_t launch_kv_append(AppendLaunch L, int num_sms, cudaStream_t stream);
 cudaError_t append_device_error(int clear, int *code);
 
+// ---- attention backward (bwd.cu) -------------------------------------------
+struct BwdLaunch {
+    // X tensors with 128-row boxes, Y tensors with 64-row boxes, each viewed
+    // as (d, S, H, B) under the 128-byte swizzle.
+    CUtensorMap tmQx, tmKx, tmVx, tmDOx, tmQy, tmKy, tmVy, tmDOy;
+    int B, Hq, Hkv, Sq, Sk, dk, dv;
+    float scale;
+    int causal;
+    const void *o, *dout;
+    int64_t o_sb, o_sh, o_ss, do_sb, do_sh, do_ss;
+    int o_bf16;
+    const float *lse, *dlse;
+    void *gq, *gk, *gv;
+    int64_t gq_sb, gq_sh, gq_ss, gk_sb, gk_sh, gk_ss, gv_sb, gv_sh, gv_ss;
+    int g_bf16;
+    ScoreMods mods;
+    bool has_mods;   // a mask or a softcap is given (sinks act through the LSE alone)
+    float *gsinks;   // NULL: not asked for
+    float *lse2, *delta;  // workspace: [B * Hq, bwd_pitch(Sq)] each
+};
+// Rows of lse2 and delta per (batch, head): Sq rounded up to the row tile.
+inline int64_t bwd_pitch(int Sq) { return ((int64_t)Sq + 127) / 128 * 128; }
+cudaError_t launch_bwd(const BwdLaunch &L, cudaStream_t stream);
+cudaError_t bwd_device_error(int clear, int *code);
+
 }  // namespace fa

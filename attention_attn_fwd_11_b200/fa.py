@@ -74,6 +74,18 @@ class KvDequantParams(ctypes.Structure):
                 ("dst", _vp), ("dst_row_stride", _i64), ("scale", ctypes.c_float)]
 
 
+_STRIDES = lambda *names: [(n + e, _i64) for n in names for e in ("_sb", "_sh", "_ss")]  # noqa: E731
+
+
+class BwdParams(ctypes.Structure):
+    _fields_ = [(n, _vp) for n in ("q", "k", "v", "o", "dout", "lse", "dlse", "gq", "gk", "gv")] + \
+        [(n, _i32) for n in ("B", "Hq", "Hkv", "Sq", "Sk", "dk", "dv")] + \
+        _STRIDES("q", "k", "v", "o", "do", "gq", "gk", "gv") + \
+        [("scale", ctypes.c_float), ("causal", _i32), ("o_dtype", _i32), ("g_dtype", _i32), ("mask", _vp)] + \
+        _STRIDES("m") + [("max_bias", ctypes.c_float), ("softcap", ctypes.c_float), ("sinks", _vp), ("gsinks", _vp),
+                         ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t)]
+
+
 class RopeParams(ctypes.Structure):
     _fields_ = [("q", _vp), ("q_out", _vp), ("q_sb", _i64), ("q_sh", _i64), ("q_ss", _i64), ("qo_sb", _i64),
                 ("qo_sh", _i64), ("qo_ss", _i64), ("k", _vp), ("k_out", _vp), ("k_sb", _i64), ("k_sh", _i64),
@@ -128,6 +140,10 @@ def load():
         lib.fa_kv_dequant.restype = _i32
         lib.fa_kv_dequant_n.argtypes = [ctypes.POINTER(KvDequantParams), _i32, _vp]
         lib.fa_kv_dequant_n.restype = _i32
+        lib.fa_bwd_workspace_size.argtypes = [ctypes.POINTER(BwdParams), ctypes.POINTER(ctypes.c_size_t)]
+        lib.fa_bwd_workspace_size.restype = _i32
+        lib.fa_bwd.argtypes = [ctypes.POINTER(BwdParams), _vp]
+        lib.fa_bwd.restype = _i32
         lib.fa_rope.argtypes = [ctypes.POINTER(RopeParams), _vp]
         lib.fa_rope.restype = _i32
         lib.fa_kv_append.argtypes = [ctypes.POINTER(KvAppendParams), _vp]
@@ -245,6 +261,88 @@ def fwd(q, k, v, scale=None, causal=False, out=None, return_lse=True, out_dtype=
     params = fwd_params(q, k, v, out, lse, scale, causal, mask, max_bias, softcap, sinks)
     _check(load().fa_fwd(ctypes.byref(params), _stream(stream)))
     return out, lse
+
+
+# ---------------------------------------------------------------- backward --
+
+def _bwd_sizes(q, k, v):
+    p = BwdParams()
+    p.B, p.Hq, p.Sq, p.dk = q.shape
+    p.Hkv, p.Sk, p.dv = v.shape[1:]
+    p.scale = 1.0
+    return p
+
+
+def bwd_workspace_bytes(q, k, v):
+    n = ctypes.c_size_t(0)
+    _check(load().fa_bwd_workspace_size(ctypes.byref(_bwd_sizes(q, k, v)), ctypes.byref(n)))
+    return n.value
+
+
+def bwd(q, k, v, o, lse, do, scale=None, causal=False, mask=None, max_bias=0.0, softcap=0.0, sinks=None, dlse=None,
+        dq=None, dk=None, dv=None, grad_dtype=torch.bfloat16, workspace=None, stream=None):
+    """Gradients of fwd() (fa_bwd), from its inputs, its output o and lse and
+    the output's gradient do [B,Hq,Sq,dv] (bf16); the same scale, causal and
+    modifiers as fwd() had.  dlse: the gradient of the log-sum-exp, if it is
+    used ([B,Hq,Sq] float32).  dq, dk, dv may be given (any strides, head dim
+    contiguous), else they are made in grad_dtype (bf16 or float32).
+    (dk, dv) head sizes: (64, 64), (128, 128), (192, 128).
+    Returns (dq, dk, dv), and with sinks (dq, dk, dv, dsinks [Hq] float32)."""
+    _need_current_device(q, k, v, o, lse, do, mask, sinks, dlse, dq, dk, dv, workspace)
+    for t in (q, k, v, do):
+        if t.dtype != torch.bfloat16 or t.dim() != 4 or t.stride(3) != 1:
+            raise ValueError("q, k, v and do must be 4-D bf16 with a contiguous last dim")
+    B, Hq, Sq, hd = q.shape
+    Hkv, Sk, vd = v.shape[1:]
+    if tuple(k.shape) != (B, Hkv, Sk, hd) or v.shape[0] != B:
+        raise ValueError("k must be [B, Hkv, Sk, dk] and v [B, Hkv, Sk, dv] with q's B and dk")
+    if tuple(o.shape) != (B, Hq, Sq, vd) or o.shape != do.shape or o.stride(3) != 1:
+        raise ValueError("o and do must be [B, Hq, Sq, dv] with a contiguous last dim")
+    for t in (lse, dlse):
+        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (B, Hq, Sq) or not t.is_contiguous()):
+            raise ValueError("lse and dlse must be contiguous float32 [B, Hq, Sq]")
+    if mask is not None and (mask.dtype != torch.float16 or mask.dim() != 4 or mask.stride(3) != 1 or
+                             mask.shape[0] not in (1, B) or mask.shape[1] not in (1, Hq) or
+                             tuple(mask.shape[2:]) != (Sq, Sk)):
+        raise ValueError("mask must be [1|B, 1|Hq, Sq, Sk] float16 with a contiguous last dim")
+    if sinks is not None and (sinks.dtype != torch.float32 or sinks.shape != (Hq,) or not sinks.is_contiguous()):
+        raise ValueError("sinks must be a contiguous float32 tensor of shape [Hq]")
+    dq, dk, dv = (torch.empty(t.shape, device=q.device, dtype=grad_dtype) if g is None else g
+                  for t, g in ((q, dq), (k, dk), (v, dv)))
+    for t, g in ((q, dq), (k, dk), (v, dv)):
+        if g.shape != t.shape or g.stride(3) != 1 or g.dtype != dq.dtype:
+            raise ValueError("dq, dk and dv must have the shapes of q, k and v, one dtype and a contiguous last dim")
+    p = _bwd_sizes(q, k, v)
+    p.q, p.k, p.v, p.o, p.dout, p.lse, p.dlse = (_ptr(t) for t in (q, k, v, o, do, lse, dlse))
+    p.gq, p.gk, p.gv = _ptr(dq), _ptr(dk), _ptr(dv)
+    p.q_sb, p.q_sh, p.q_ss = q.stride()[:3]
+    p.k_sb, p.k_sh, p.k_ss = k.stride()[:3]
+    p.v_sb, p.v_sh, p.v_ss = v.stride()[:3]
+    p.o_sb, p.o_sh, p.o_ss = o.stride()[:3]
+    p.do_sb, p.do_sh, p.do_ss = do.stride()[:3]
+    p.gq_sb, p.gq_sh, p.gq_ss = dq.stride()[:3]
+    p.gk_sb, p.gk_sh, p.gk_ss = dk.stride()[:3]
+    p.gv_sb, p.gv_sh, p.gv_ss = dv.stride()[:3]
+    p.scale = 1.0 / math.sqrt(hd) if scale is None else scale
+    p.causal = 1 if causal else 0
+    p.o_dtype, p.g_dtype = _odt(o.dtype), _odt(dq.dtype)
+    if mask is not None:
+        p.mask = _ptr(mask)
+        p.m_sb = 0 if mask.shape[0] == 1 else mask.stride(0)
+        p.m_sh = 0 if mask.shape[1] == 1 else mask.stride(1)
+        p.m_ss = mask.stride(2)
+    p.max_bias, p.softcap = max_bias, softcap
+    dsinks = None
+    if sinks is not None:
+        dsinks = torch.empty_like(sinks)
+        p.sinks, p.gsinks = _ptr(sinks), _ptr(dsinks)
+    if workspace is None:
+        n = ctypes.c_size_t(0)
+        _check(load().fa_bwd_workspace_size(ctypes.byref(p), ctypes.byref(n)))
+        workspace = torch.empty(max(n.value, 256), device=q.device, dtype=torch.uint8)
+    p.workspace, p.workspace_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
+    _check(load().fa_bwd(ctypes.byref(p), _stream(stream)))
+    return (dq, dk, dv) if sinks is None else (dq, dk, dv, dsinks)
 
 
 # ------------------------------------------------------------- paged decode --

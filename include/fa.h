@@ -137,6 +137,70 @@ typedef struct {
 fa_status fa_fwd(const fa_fwd_params *p, void *stream);
 
 /*
+ * fa_bwd -- the gradients of fa_fwd, from its inputs, its output and its
+ * log-sum-exp (the probabilities are recomputed):
+ *   P_ij = exp(s_ij - lse_i),  D_i = dO_i . O_i - dlse_i,
+ *   dS_ij = P_ij (dO_i . V_j - D_i) (ds/dz)_ij,
+ *   gq_i = scale sum_j dS_ij K_j,  gk_j = scale sum_i dS_ij Q_i,
+ *   gv_j = sum_i P_ij dO_i
+ * with s the scores of fa_fwd after its modifiers and ds/dz = softcap (1 -
+ * tanh^2(scale q.k)) under a softcap, else 1.
+ *   q, k, v, o, lse, and every shape, stride, scale, causal and modifier
+ *     field: as fa_fwd had them (lse is needed; with sinks it includes them).
+ *     o is bf16 or fp32 (o_dtype).  dout: [B, Hq, Sq, dv] bf16, strides as
+ *     for q.
+ *   dlse: NULL, or [B, Hq, Sq] fp32 contiguous: the gradient that reaches
+ *     the log-sum-exp itself.
+ *   gq: [B, Hq, Sq, dk], gk: [B, Hkv, Sk, dk], gv: [B, Hkv, Sk, dv] in
+ *     g_dtype, strides multiples of 8 (bf16) or 4 (fp32), each sequence
+ *     stride >= the width, bases 16-byte aligned.  A KV head's gradients are
+ *     the sums over its query heads.  They may not overlap the inputs.
+ *   gsinks: NULL, or [Hq] fp32 (needs sinks): the gradient of the sinks,
+ *     -sum over rows of exp(sink_h - lse) D.
+ *   Rows with no visible key (lse -inf) get gq = 0 and add nothing.  There is
+ *   no gradient of the mask.  Keys that no query sees get gk = gv = 0.
+ *   workspace: at least fa_bwd_workspace_size() bytes, 256-byte aligned,
+ *     overwritten on every call.
+ * Scores, P, D and every sum are fp32; P and dS are rounded once to bf16, the
+ * operand type of the products that follow.  No sum is made with atomics:
+ * equal inputs give equal bits.
+ * Supported (dk, dv): (64, 64), (128, 128), (192, 128); other pairs of fa_fwd
+ * are FA_ERR_UNSUPPORTED.  Values in rows that a mask hides must be finite
+ * (0 * NaN is NaN).  B == 0 is a no-op (but for gsinks, written as 0); Sq == 0
+ * writes gk = gv = 0, Sk == 0 gq = 0.
+ */
+typedef struct {
+    const void *q, *k, *v, *o, *dout;
+    const float *lse, *dlse;
+    void *gq, *gk, *gv;
+    int B, Hq, Hkv, Sq, Sk, dk, dv;
+    int64_t q_sb, q_sh, q_ss;
+    int64_t k_sb, k_sh, k_ss;
+    int64_t v_sb, v_sh, v_ss;
+    int64_t o_sb, o_sh, o_ss;
+    int64_t do_sb, do_sh, do_ss;
+    int64_t gq_sb, gq_sh, gq_ss;
+    int64_t gk_sb, gk_sh, gk_ss;
+    int64_t gv_sb, gv_sh, gv_ss;
+    float scale;
+    int causal;
+    int o_dtype, g_dtype; /* fa_dtype */
+    /* score modifiers (zero / NULL: off), as in fa_fwd */
+    const void *mask; /* f16 */
+    int64_t m_sb, m_sh, m_ss;
+    float max_bias;
+    float softcap;
+    const float *sinks;
+    float *gsinks;
+    void *workspace;
+    size_t workspace_bytes;
+} fa_bwd_params;
+
+/* Workspace bytes for these shapes; reads no pointer field. */
+fa_status fa_bwd_workspace_size(const fa_bwd_params *p, size_t *bytes);
+fa_status fa_bwd(const fa_bwd_params *p, void *stream);
+
+/*
  * fa_prefill_paged -- chunked prefill over a paged KV cache: the decode call
  * of fa_decode_paged with Sq > 1 new query rows per sequence, computed by the
  * prefill kernel with its key tiles gathered through the block table.
