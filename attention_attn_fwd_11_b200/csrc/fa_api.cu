@@ -397,7 +397,7 @@ fa_status check_bwd(const fa_bwd_params *p) {
     return FA_OK;
 }
 
-size_t bwd_row_bytes(const fa_bwd_params *p) {  // of the row LSE, and of D
+size_t bwd_row_bytes(const fa_bwd_params *p) {  // of the row LSE, of D, and a quarter of both as bf16 pieces
     const size_t n = (size_t)p->B * p->Hq * (size_t)fa::bwd_pitch(p->Sq) * sizeof(float);
     return (n + 255) & ~size_t(255);
 }
@@ -1028,7 +1028,7 @@ fa_status fa_bwd_workspace_size(const fa_bwd_params *p, size_t *bytes) {
     fa_status st = check_bwd(p);
     if (st != FA_OK) return st;
     if (!bytes) return fail(FA_ERR_INVALID_ARG, "fa_bwd_workspace_size: bytes is NULL");
-    *bytes = 2 * bwd_row_bytes(p);
+    *bytes = 6 * bwd_row_bytes(p);
     return FA_OK;
 }
 
@@ -1059,7 +1059,7 @@ fa_status fa_bwd(const fa_bwd_params *p, void *stream) {
                     p->m_sh < 0 || p->m_sb < 0))
         return fail(FA_ERR_INVALID_ARG,
                     "fa_bwd: mask must be 16-byte aligned, its strides multiples of 8 elements, m_ss >= Sk");
-    const size_t each = bwd_row_bytes(p), need = 2 * each;
+    const size_t each = bwd_row_bytes(p), need = 6 * each;
     if (need > 0 && (!p->workspace || p->workspace_bytes < need || ((uintptr_t)p->workspace & 255u)))
         return fail(FA_ERR_WORKSPACE, "fa_bwd: workspace needs %zu bytes, 256-byte aligned", need);
     if (!get_encoder()) return fail(FA_ERR_CUDA, "fa_bwd: cuTensorMapEncodeTiled is not available");
@@ -1069,7 +1069,7 @@ fa_status fa_bwd(const fa_bwd_params *p, void *stream) {
     const auto both = [&](CUtensorMap *x, CUtensorMap *y, const void *t, int d, int S, int H, int64_t ss, int64_t sh,
                           int64_t sb, const char *name) {
         fa_status r = encode_4d(x, t, d, S, H, p->B, ss, sh, sb, 128, name);
-        return r == FA_OK ? encode_4d(y, t, d, S, H, p->B, ss, sh, sb, 64, name) : r;
+        return r == FA_OK ? encode_4d(y, t, d, S, H, p->B, ss, sh, sb, fa::bwd_walk(p->dk), name) : r;
     };
     if (rows) {
         st = both(&L.tmQx, &L.tmQy, p->q, p->dk, p->Sq, p->Hq, p->q_ss, p->q_sh, p->q_sb, "fa_bwd q");
@@ -1127,10 +1127,11 @@ fa_status fa_bwd(const fa_bwd_params *p, void *stream) {
         L.mods.log2_m0 = -p->max_bias / (float)n2;
         L.mods.log2_m1 = -p->max_bias / 2.f / (float)n2;
     }
-    L.has_mods = p->mask || p->softcap > 0.f;
+    L.has_mods = p->mask || p->softcap > 0.f || p->scale < 1e-30f;
     L.gsinks = p->gsinks;
-    L.lse2 = static_cast<float *>(p->workspace);
-    L.delta = reinterpret_cast<float *>(static_cast<char *>(p->workspace) + each);
+    L.nlse2 = static_cast<float *>(p->workspace);
+    L.ndelta = reinterpret_cast<float *>(static_cast<char *>(p->workspace) + each);
+    L.ext = static_cast<char *>(p->workspace) + 2 * each;
     cudaError_t e = fa::launch_bwd(L, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "fa_bwd: launch");
     return FA_OK;

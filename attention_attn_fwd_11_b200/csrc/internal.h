@@ -191,8 +191,8 @@ cudaError_t append_device_error(int clear, int *code);
 
 // ---- attention backward (bwd.cu) -------------------------------------------
 struct BwdLaunch {
-    // X tensors with 128-row boxes, Y tensors with 64-row boxes, each viewed
-    // as (d, S, H, B) under the 128-byte swizzle.
+    // The resident side (x) with 128-row boxes, the walked side (y) with
+    // bwd_walk(dk) rows, each viewed as (d, S, H, B) under the 128-byte swizzle.
     CUtensorMap tmQx, tmKx, tmVx, tmDOx, tmQy, tmKy, tmVy, tmDOy;
     int B, Hq, Hkv, Sq, Sk, dk, dv;
     float scale;
@@ -205,12 +205,19 @@ struct BwdLaunch {
     int64_t gq_sb, gq_sh, gq_ss, gk_sb, gk_sh, gk_ss, gv_sb, gv_sh, gv_ss;
     int g_bf16;
     ScoreMods mods;
-    bool has_mods;   // a mask or a softcap is given (sinks act through the LSE alone)
+    // A mask or a softcap is given (sinks act through the LSE alone); also set
+    // for scales below 1e-30, whose LSE / scale may leave fp32's range.
+    bool has_mods;
     float *gsinks;   // NULL: not asked for
-    float *lse2, *delta;  // workspace: [B * Hq, bwd_pitch(Sq)] each
+    float *nlse2, *ndelta;  // workspace: [B * Hq, bwd_pitch(Sq)] each,
+    void *ext;              // and as many 16-byte rows
 };
-// Rows of lse2 and delta per (batch, head): Sq rounded up to the row tile.
-inline int64_t bwd_pitch(int Sq) { return ((int64_t)Sq + 127) / 128 * 128; }
+// Rows of nlse2 and ndelta per (batch, head): Sq rounded up to whole tiles,
+// walked (128 or 96) and the resident one (128) alike.
+inline int64_t bwd_pitch(int Sq) { return ((int64_t)Sq + 383) / 384 * 384; }
+// Rows of a walked tile: 128, or what TMEM holds beside 192 + 128 columns of
+// dK and dV.
+constexpr int bwd_walk(int dk) { return dk == 192 ? 96 : 128; }
 cudaError_t launch_bwd(const BwdLaunch &L, cudaStream_t stream);
 cudaError_t bwd_device_error(int clear, int *code);
 

@@ -406,6 +406,22 @@ FA_DEV void mma_ts4_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint
         : "memory");
 }
 
+// Two TMEM-A MMAs from one elected lane: A steps by AO columns, the B
+// descriptor by BO (16-byte units).
+template <uint32_t AO, uint32_t BO>
+FA_DEV void mma_ts2_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t acc0) {
+    asm volatile(
+        "{\n\t.reg .pred p, q, e;\n\t.reg .b32 a1;\n\t.reg .b64 b1;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.eq.b32 q, 0, 0;\n\t"
+        "add.u32 a1, %1, %5;\n\tadd.s64 b1, %2, %6;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, q;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(acc0), "n"(AO), "n"(BO)
+        : "memory");
+}
+
 // Four TMEM-A MMAs from one elected lane: A at columns 0, A1, A2 and A3 from
 // a_tmem, the B descriptor stepping by BO (16-byte units).
 template <uint32_t A1, uint32_t A2, uint32_t A3, uint32_t BO>
@@ -456,6 +472,18 @@ FA_DEV uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo_bytes, uint32_t sbo_byt
     d |= (uint64_t)((sbo_bytes >> 4) & 0x3FFFu) << 32;
     d |= (uint64_t)1 << 46;  // descriptor version for sm_100
     d |= (uint64_t)2 << 61;  // swizzle mode: 128 B
+    return d;
+}
+
+// Shared-memory matrix descriptor of a K-major operand without swizzle: core
+// matrices of 8 rows x 16 bytes, 128 contiguous bytes each; lbo = byte
+// distance to the next one along K, sbo = to the next 8 rows.
+FA_DEV uint64_t sdesc_plain(uint32_t saddr, uint32_t lbo_bytes, uint32_t sbo_bytes) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+    d |= (uint64_t)((lbo_bytes >> 4) & 0x3FFFu) << 16;
+    d |= (uint64_t)((sbo_bytes >> 4) & 0x3FFFu) << 32;
+    d |= (uint64_t)1 << 46;  // descriptor version for sm_100
     return d;
 }
 
@@ -570,6 +598,28 @@ FA_DEV uint64_t f2_mul(uint64_t a, uint64_t b) {
     uint64_t d;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
+}
+// 2^a and 2^b on the FMA pipe, for where the exponential unit is the bound:
+// x = n + f with n the nearest integer (added and taken off again at 1.5 *
+// 2^23, whose low bits then hold n) and |f| <= 1/2, 2^f by a polynomial of
+// degree 4 fitted to the least relative error with p(0) = 1 (2.9e-6), and n
+// added to the exponent bits.  x below -127 counts as -127: f is then 0 and
+// the bits add up to exactly +0, so 2^-inf = 0.  x must be below 127.
+FA_DEV void exp2_poly2(float a, float b, float &ra, float &rb) {
+    const uint64_t magic = f2_pack(12582912.f, 12582912.f), minus = f2_pack(-12582912.f, -12582912.f);
+    const uint64_t x = f2_pack(fmaxf(a, -127.f), fmaxf(b, -127.f));
+    const uint64_t r = f2_add(x, magic);
+    const uint64_t f = f2_fma(f2_add(r, minus), f2_pack(-1.f, -1.f), x);
+    uint64_t p = f2_fma(f, f2_pack(0.009582852944731712f, 0.009582852944731712f),
+                        f2_pack(0.055906426161527634f, 0.055906426161527634f));
+    p = f2_fma(p, f, f2_pack(0.24024099111557007f, 0.24024099111557007f));
+    p = f2_fma(p, f, f2_pack(0.6931241750717163f, 0.6931241750717163f));
+    p = f2_fma(p, f, f2_pack(1.f, 1.f));
+    float p0, p1, n0, n1;
+    f2_unpack(p, p0, p1);
+    f2_unpack(r, n0, n1);
+    ra = __uint_as_float(__float_as_uint(p0) + (__float_as_uint(n0) << 23));
+    rb = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(n1) << 23));
 }
 // Three-input maximum (one instruction).
 FA_DEV float fmax3(float a, float b, float c) {
