@@ -54,31 +54,37 @@ namespace {
 
 __device__ int g_bwd_err;
 
+struct BwdGrad {  // an output [B, H, S, d]
+    char *p;
+    int64_t sb, sh, ss;
+};
+
 struct BwdArgs {
-    int Hq, Hkv, Sq, Sk, causal;
+    int B, Hq, Hkv, Sq, Sk, causal;
     float scale, scale_log2;
     ScoreMods mods;
     const float *nlse2, *ndelta;  // -LSE in base 2 and -D of every row
     const uint4 *ext;             // the two of a row as the B side of the extra step (see BwdCfg)
     int64_t pitch;                // rows per (batch, head) of the three
-    int outer;      // 128-row tiles of the resident side
-    char *g1, *g2;  // dK and dV, or dQ
-    int64_t g1_sb, g1_sh, g1_ss, g2_sb, g2_sh, g2_ss;
+    int kv_items, items;          // 128-key tiles of every KV head, then 128-query tiles of every head
+    int *next;                    // first item that no CTA has taken
+    BwdGrad gq, gk, gv;
     int g_bf16;
 };
 
 // Shared and tensor memory of one walk.  TMEM holds the accumulators and one
 // S and one T tile.  Where there is room P and dS get columns of their own, so
-// that S and T are free as soon as they are read, and after that the resident
-// operands: an operand in TMEM saves its reads of shared memory, which at 8 KB
-// a product of 64 cycles are all that memory gives.
+// that S and T are free as soon as they are read.
 template <int DK, int DV, bool KV, bool MODS>
 struct BwdCfg {
     static constexpr int BN = bwd_walk(DK);
     // dK / dV without modifiers: LSE and D enter the products as one more
     // step of 16 columns.
     static constexpr bool EXT = KV && !MODS;
-    static constexpr int NST1 = DK == 64 ? 4 : KV ? 2 : 3, NST2 = DK == 64 ? 4 : 2;  // stages of Y1 and of Y2
+    // Stages of Y1 and of Y2.  dQ needs the third of Y1 (K: the next tile's S
+    // comes before this tile's product with it) more than the second of Y2.
+    static constexpr int NST1 = DK == 64 ? 4 : KV ? 2 : 3;
+    static constexpr int NST2 = DK == 64 ? 4 : !KV && DK == 192 ? 1 : 2;
     static constexpr int X_CHUNK = 128 * 128, Y_CHUNK = BN * 128;  // bytes of a 64-column chunk
     static constexpr int X1_BYTES = 128 * DK * 2, X2_BYTES = 128 * DV * 2;
     static constexpr int Y1_BYTES = BN * DK * 2, Y2_BYTES = BN * DV * 2;
@@ -87,274 +93,358 @@ struct BwdCfg {
     static constexpr int OFF_ROW = 2 * EXT_A;
     static constexpr int OFF_X1 = (OFF_ROW + NST1 * ROW_BYTES + 1023) / 1024 * 1024;
     static constexpr int OFF_X2 = OFF_X1 + X1_BYTES;
-    // The last stage of Y1 may lie where the operand was that moved to TMEM.
-    static constexpr bool REUSE = !KV && DK > 64;
-    static constexpr int X2_ROOM = REUSE && DK == 192 ? Y1_BYTES : X2_BYTES;
-    static constexpr int OFF_Y1 = OFF_X2 + X2_ROOM;
-    static constexpr int OFF_Y2 = OFF_Y1 + (NST1 - REUSE) * Y1_BYTES;
-    static constexpr int OFF_BAR = OFF_Y2 + NST2 * Y2_BYTES;
-    static constexpr int SMEM_BYTES = OFF_BAR + 256 + 1024;  // barriers + alignment slack
-    FA_DEV static uint32_t y1(int s) {  // offset of stage s
-        return REUSE && s == NST1 - 1 ? (DK == 192 ? OFF_X2 : OFF_X1) : OFF_Y1 + s * Y1_BYTES;
-    }
-    static constexpr int WARPS = BN / 8;            // of elementwise work: four for 32 columns
-    static constexpr int THREADS = 128 + 32 * WARPS;
+    static constexpr int OFF_Y1 = OFF_X2 + X2_BYTES;
+    static constexpr int OFF_Y2 = OFF_Y1 + NST1 * Y1_BYTES;
+    static constexpr int END = OFF_Y2 + NST2 * Y2_BYTES;
+    static constexpr int WARPS = BN / 8;  // of elementwise work: four for 32 columns
     static constexpr int TMEM_COLS = 512;
     static constexpr int ACC = DK + (KV ? DV : 0);
-    static constexpr int OWN = (KV ? BN : BN / 2);  // columns of separate P and dS
-    static constexpr bool ALIAS = ACC + 2 * BN + OWN > TMEM_COLS;
-    static constexpr int T_A1 = 0, T_A2 = DK, T_S = ACC, T_T = T_S + BN;
+    // S and T lie behind dK and dV in both walks: dQ's first products may run
+    // while the last dK and dV are read out.
+    static constexpr int T_A1 = 0, T_A2 = DK, T_S = DK + DV, T_T = T_S + BN, T_END = T_T + BN;
     // P over S and dS over T (each warpgroup in its own columns), or apart
+    static constexpr bool ALIAS = KV && T_END + BN > TMEM_COLS;
     static constexpr int WG_COLS = ALIAS ? 32 : 16;  // from one warpgroup's P or dS to the next
-    static constexpr int T_P = ALIAS ? T_S : T_T + BN;
-    static constexpr int T_D = ALIAS ? T_T : T_T + BN + (KV ? BN / 2 : 0);
-    static constexpr int T_X = ALIAS ? T_T + BN : T_D + BN / 2;
-    static constexpr bool X1_TMEM = T_X + DK / 2 <= TMEM_COLS;
-    static constexpr int T_X2 = T_X + (X1_TMEM ? DK / 2 : 0);
-    static constexpr bool X2_TMEM = T_X2 + DV / 2 <= TMEM_COLS;
-    static constexpr bool X_TMEM = X1_TMEM || X2_TMEM;
-    static_assert(T_X <= TMEM_COLS, "TMEM budget");
-    static_assert(!REUSE || (DK == 192 ? X2_TMEM : X1_TMEM && X1_BYTES >= Y1_BYTES), "the reused operand is in TMEM");
+    static constexpr int T_P = ALIAS ? T_S : T_END;
+    static constexpr int T_D = ALIAS ? T_T : KV ? T_END + BN / 2 : T_END + BN / 2 <= TMEM_COLS ? T_END : DK;
+    static_assert(T_END <= TMEM_COLS && T_D + (ALIAS ? BN : BN / 2) <= TMEM_COLS, "TMEM budget");
+    static_assert(T_D >= T_END || ALIAS || T_D + BN / 2 <= T_S, "dS apart from S");
+    // Barriers of this walk (each kind of item has its own set).
+    static constexpr int FULL1 = 10, EMPTY1 = FULL1 + NST1, FULL2 = EMPTY1 + NST1, EMPTY2 = FULL2 + NST2;
+    static constexpr int BARS = EMPTY2 + NST2;
+};
+
+enum { B_X1FULL, B_X2FULL, B_X1FREE, B_X2FREE, B_SFULL, B_TFULL, B_SREAD, B_TREAD, B_PREADY, B_DSREADY };
+
+template <int DK, int DV, bool MODS>
+struct BwdKernel {
+    using CK = BwdCfg<DK, DV, true, MODS>;
+    using CQ = BwdCfg<DK, DV, false, MODS>;
+    static constexpr int THREADS = 128 + 32 * CK::WARPS;
+    static constexpr int OFF_BAR = CK::END > CQ::END ? CK::END : CQ::END;
+    // Barriers: the item ring (full, empty), the end of a walk's products, of
+    // all of them, the workers' change from dK / dV to dQ, then both kinds' sets.
+    static constexpr int BAR_DONE = 4, BAR_END = 5, BAR_MOVED = 6, BAR_KV = 7, BAR_Q = BAR_KV + CK::BARS, BARS = BAR_Q + CQ::BARS;
+    static constexpr int SMEM_BYTES = OFF_BAR + 8 * BARS + 32 + 1024;  // item ring, TMEM address, flag; alignment slack
     static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 };
 
-enum { B_XFULL, B_XTMEM, B_SFULL, B_TFULL, B_SREAD, B_TREAD, B_PREADY, B_DSREADY, B_DONE, B_RING };
+// One item: a 128-row tile x0 of (b, h) and its walk over tiles y_first ..
+// y_first + n_y - 1, for dK / dV once per head of the group.
+struct BwdItem {
+    int b, h, x0, y_first, n_y, n;
+};
 
-// 64 columns of this thread's row of a swizzled chunk (128-byte rows) to 32
-// TMEM columns.
-FA_DEV void chunk_to_tmem(const uint8_t *chunk, int row, uint32_t taddr) {
-    uint32_t r[32];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const uint4 w = *reinterpret_cast<const uint4 *>(chunk + row * 128 + ((j ^ (row & 7)) << 4));
-        r[4 * j] = w.x, r[4 * j + 1] = w.y, r[4 * j + 2] = w.z, r[4 * j + 3] = w.w;
+// Items in the order in which they are taken: dK / dV, then dQ, each with the
+// longest walks first (key tile 0 sees the most queries, the last query tile
+// the most keys), so that what is taken last is short.
+template <bool KV, int BN>
+FA_DEV BwdItem bwd_item(const BwdArgs &a, int i) {
+    BwdItem it;
+    const int H = KV ? a.Hkv : a.Hq;
+    const unsigned per = (unsigned)(a.B * H), idx = (unsigned)(KV ? i : i - a.kv_items);
+    const int bh = (int)(idx % per), turn = (int)(idx / per);
+    const int xt = KV ? turn : (a.Sq + 127) / 128 - 1 - turn;
+    it.b = bh / H;
+    it.h = bh % H;
+    it.x0 = xt * 128;
+    const int shift = a.Sk - a.Sq;  // causal: key j is visible to query i iff j <= i + shift
+    it.y_first = 0;
+    if (KV) {
+        if (a.causal) it.y_first = max(0, it.x0 - shift) / BN;
+        it.n_y = max(0, (a.Sq + BN - 1) / BN - it.y_first);
+        it.n = it.n_y * (a.Hq / a.Hkv);
+    } else {
+        int last = a.Sk;  // keys visible to the tile's last row
+        if (a.causal) last = min(last, min(a.Sq, it.x0 + 128) + shift);
+        it.n_y = last <= 0 ? 0 : (last + BN - 1) / BN;
+        it.n = it.n_y;
     }
-    tmem_st32(taddr, r);
+    return it;
 }
+
+// A position in a ring of N stages: the stage and the parity of its use.
+template <int N>
+struct Ring {
+    int s = 0;
+    uint32_t ph = 0;
+    FA_DEV void next() {
+        if (++s == N) s = 0, ph ^= 1u;
+    }
+};
 
 // Of every eight exponentials, this many go to the FMA pipe (exp2_poly2).
 constexpr int kPolyOf8 = 2;
 
-template <int DK, int DV, bool KV, bool MODS>
-__global__ void __launch_bounds__(BwdCfg<DK, DV, KV, MODS>::THREADS, 1)
-bwd_tile_kernel(const __grid_constant__ CUtensorMap tmX1, const __grid_constant__ CUtensorMap tmX2,
-                const __grid_constant__ CUtensorMap tmY1, const __grid_constant__ CUtensorMap tmY2, const BwdArgs a) {
-    using C = BwdCfg<DK, DV, KV, MODS>;
-    constexpr int BN = C::BN, NST1 = C::NST1, NST2 = C::NST2;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const uint32_t sbase = smem_u32(smem), sX1 = sbase + C::OFF_X1, sX2 = sbase + C::OFF_X2, sY2 = sbase + C::OFF_Y2;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
-    const uint32_t bar0 = smem_u32(bars);
-    auto bar = [&](int i) -> uint32_t { return bar0 + 8u * (uint32_t)i; };
-    auto full1 = [&](int s) { return bar(B_RING + s); };
-    auto empty1 = [&](int s) { return bar(B_RING + NST1 + s); };
-    auto full2 = [&](int s) { return bar(B_RING + 2 * NST1 + s); };
-    auto empty2 = [&](int s) { return bar(B_RING + 2 * NST1 + NST2 + s); };
-    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + 28);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
-    static_assert(B_RING + 2 * (NST1 + NST2) <= 28, "barrier slots");
+// What every role of a CTA shares.
+struct BwdCta {
+    uint8_t *smem;
+    uint32_t sbase, bar0, tmem;
+    volatile int *abort_flag;
+    FA_DEV uint32_t bar(int i) const { return bar0 + 8u * (uint32_t)i; }
+    FA_DEV bool wait(int i, uint32_t parity) const {
+        return mbar_wait_warp_fast(bar(i), parity, abort_flag, &g_bwd_err);
+    }
+    FA_DEV bool wait1(int i, uint32_t parity) const { return mbar_wait(bar(i), parity, abort_flag, &g_bwd_err); }
+};
 
-    const int warp = threadIdx.x >> 5;
-    const int lane = threadIdx.x & 31;
-    const int group = a.Hq / a.Hkv;
-    const int H = KV ? a.Hkv : a.Hq;
-    // The tiles with the longest walks first: key tile 0 sees the most
-    // queries, the last query tile the most keys.
-    const int bh = (int)(blockIdx.x % (unsigned)(gridDim.x / a.outer));
-    const int xt = KV ? (int)(blockIdx.x / (gridDim.x / a.outer)) : a.outer - 1 - (int)(blockIdx.x / (gridDim.x / a.outer));
-    const int b = bh / H, h = bh % H;
-    const int x0 = xt * 128;
-    const int shift = a.Sk - a.Sq;  // causal: key j is visible to query i iff j <= i + shift
-    // Walk: tiles y_first .. y_first + n_y - 1, for dK / dV once per head of
-    // the group.
-    int y_first = 0, n_y;
-    if (KV) {
-        if (a.causal) y_first = max(0, x0 - shift) / BN;
-        n_y = max(0, (a.Sq + BN - 1) / BN - y_first);
-    } else {
-        int last = a.Sk;  // keys visible to the tile's last row
-        if (a.causal) last = min(last, min(a.Sq, x0 + 128) + shift);
-        n_y = last <= 0 ? 0 : (last + BN - 1) / BN;
-    }
-    const int n = KV ? n_y * group : n_y;
+// ---- warp 0, one lane: TMA producer ----------------------------------------
+template <class C>
+struct BwdProducer {
+    Ring<C::NST1> r1;
+    Ring<C::NST2> r2;
+    int issued1 = 0, issued2 = 0, walks = 0;  // tiles asked for; items whose X1 and X2 were
+    bool x1_pending = false;                  // X1 of one more was
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < B_RING + 2 * (NST1 + NST2); ++i)
-            mbar_init(bar(i), i == B_XTMEM || (i >= B_SREAD && i <= B_DSREADY) ? C::WARPS : 1);
-        *abort_flag = 0;
-        fence_barrier_init();
-    }
-    if (C::EXT) {
-        // A side of the extra step: row = 1 in columns 0 .. 2 for S (the three
-        // pieces of the LSE), 3 .. 5 for T (those of D); the second half of
-        // its 16 columns, on both sides, is zeros.
-        uint4 *e = reinterpret_cast<uint4 *>(smem);
-        for (int i = threadIdx.x; i < 2 * C::EXT_A / 16; i += C::THREADS)
-            e[i] = (i & 128) ? make_uint4(0, 0, 0, 0)
-                   : i < 256 ? make_uint4(0x3f803f80u, 0x3f80u, 0, 0)
-                             : make_uint4(0, 0x3f800000u, 0x3f803f80u, 0);
-        for (int i = threadIdx.x; i < NST1 * BN; i += C::THREADS)
-            reinterpret_cast<uint4 *>(smem + C::OFF_ROW + (i / BN) * C::ROW_BYTES)[BN + i % BN] = make_uint4(0, 0, 0, 0);
-        fence_proxy_async_smem();
-    }
-    if (warp == 1) {
-        tmem_alloc(smem_u32(tmem_holder), C::TMEM_COLS);
-        tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_holder;
-
-    if (warp == 0) {
-        // ------------------------------------------------ TMA producer --
-        if (lane == 0 && n > 0) {
-            prefetch_tmap(&tmX1);
-            prefetch_tmap(&tmX2);
-            prefetch_tmap(&tmY1);
-            prefetch_tmap(&tmY2);
-            mbar_arrive_expect_tx(bar(B_XFULL), C::X1_BYTES + C::X2_BYTES);
-            for (int c = 0; c < DK / 64; ++c) tma_load_4d(sX1 + c * C::X_CHUNK, &tmX1, bar(B_XFULL), c * 64, x0, h, b);
-            for (int c = 0; c < DV / 64; ++c) tma_load_4d(sX2 + c * C::X_CHUNK, &tmX2, bar(B_XFULL), c * 64, x0, h, b);
-            int issued1 = 0, issued2 = 0, y = 0, hy = KV ? h * group : h / group;
-            for (int t = 0; t < n; ++t) {
-                const int s1 = t % NST1, s2 = t % NST2;
-                const int y0 = (y_first + y) * BN;
-                if (!mbar_wait(empty1(s1), ((uint32_t)(t / NST1) & 1u) ^ 1u, abort_flag, &g_bwd_err)) break;
-                if (C::REUSE && t == NST1 - 1 && !mbar_wait(bar(B_XTMEM), 0, abort_flag, &g_bwd_err)) break;
-                mbar_arrive_expect_tx(full1(s1), C::Y1_BYTES + (C::EXT ? C::ROW_BYTES / 2 : C::ROW_BYTES));
-                for (int c = 0; c < DK / 64; ++c)
-                    tma_load_4d(sbase + C::y1(s1) + c * C::Y_CHUNK, &tmY1, full1(s1), c * 64, y0, hy, b);
-                if (KV) {
-                    const int64_t row = ((int64_t)b * a.Hq + hy) * a.pitch + y0;
-                    const uint32_t sr = sbase + C::OFF_ROW + s1 * C::ROW_BYTES;
-                    if (C::EXT) {
-                        bulk_load(sr, a.ext + row, BN * 16, full1(s1));
-                    } else {
-                        bulk_load(sr, a.nlse2 + row, BN * 4, full1(s1));
-                        bulk_load(sr + BN * 4, a.ndelta + row, BN * 4, full1(s1));
-                    }
+    template <int DK, int DV, bool KV>
+    FA_DEV bool item(const BwdCta &c, const BwdArgs &a, const BwdItem &it, int bars, const CUtensorMap *tmX1,
+                     const CUtensorMap *tmX2, const CUtensorMap *tmY1, const CUtensorMap *tmY2) {
+        if (it.n == 0) return true;
+        const int group = a.Hq / a.Hkv;
+        const uint32_t sb = c.sbase;
+        // X of the walk before is free when its last S, its last T is done.
+        const uint32_t px = ((uint32_t)walks & 1u) ^ 1u;
+        int y = 0, hy = KV ? it.h * group : it.h / group;
+        for (int t = 0; t < it.n; ++t) {
+            const int y0 = (it.y_first + y) * C::BN;
+            if (t == 0) {
+                if (!c.wait1(bars + B_X1FREE, px)) return false;
+                const uint32_t xf = c.bar(bars + B_X1FULL);
+                mbar_arrive_expect_tx(xf, C::X1_BYTES);
+                x1_pending = true;
+                for (int i = 0; i < DK / 64; ++i)
+                    tma_load_4d(sb + C::OFF_X1 + i * C::X_CHUNK, tmX1, xf, i * 64, it.x0, it.h, it.b);
+            }
+            if (!c.wait1(bars + C::EMPTY1 + r1.s, r1.ph ^ 1u)) return false;
+            const uint32_t f1 = c.bar(bars + C::FULL1 + r1.s);
+            mbar_arrive_expect_tx(f1, C::Y1_BYTES + (C::EXT ? C::ROW_BYTES / 2 : C::ROW_BYTES));
+            for (int i = 0; i < DK / 64; ++i)
+                tma_load_4d(sb + C::OFF_Y1 + r1.s * C::Y1_BYTES + i * C::Y_CHUNK, tmY1, f1, i * 64, y0, hy, it.b);
+            if (KV) {
+                const int64_t row = ((int64_t)it.b * a.Hq + hy) * a.pitch + y0;
+                const uint32_t sr = sb + C::OFF_ROW + r1.s * C::ROW_BYTES;
+                if (C::EXT) {
+                    bulk_load(sr, a.ext + row, C::BN * 16, f1);
+                } else {
+                    bulk_load(sr, a.nlse2 + row, C::BN * 4, f1);
+                    bulk_load(sr + C::BN * 4, a.ndelta + row, C::BN * 4, f1);
                 }
-                issued1 = t + 1;
-                if (!mbar_wait(empty2(s2), ((uint32_t)(t / NST2) & 1u) ^ 1u, abort_flag, &g_bwd_err)) break;
-                mbar_arrive_expect_tx(full2(s2), C::Y2_BYTES);
-                for (int c = 0; c < DV / 64; ++c)
-                    tma_load_4d(sY2 + s2 * C::Y2_BYTES + c * C::Y_CHUNK, &tmY2, full2(s2), c * 64, y0, hy, b);
-                issued2 = t + 1;
-                if (++y == n_y) y = 0, ++hy;
             }
-            if (*abort_flag) {
-                mbar_wait_drain(bar(B_XFULL), 0);
-                for (int t = max(0, issued1 - NST1); t < issued1; ++t)
-                    mbar_wait_drain(full1(t % NST1), (uint32_t)(t / NST1) & 1u);
-                for (int t = max(0, issued2 - NST2); t < issued2; ++t)
-                    mbar_wait_drain(full2(t % NST2), (uint32_t)(t / NST2) & 1u);
+            r1.next();
+            ++issued1;
+            if (t == 0) {
+                if (!c.wait1(bars + B_X2FREE, px)) return false;
+                const uint32_t xf = c.bar(bars + B_X2FULL);
+                mbar_arrive_expect_tx(xf, C::X2_BYTES);
+                for (int i = 0; i < DV / 64; ++i)
+                    tma_load_4d(sb + C::OFF_X2 + i * C::X_CHUNK, tmX2, xf, i * 64, it.x0, it.h, it.b);
+                ++walks;
+                x1_pending = false;
             }
+            if (!c.wait1(bars + C::EMPTY2 + r2.s, r2.ph ^ 1u)) return false;
+            const uint32_t f2 = c.bar(bars + C::FULL2 + r2.s);
+            mbar_arrive_expect_tx(f2, C::Y2_BYTES);
+            for (int i = 0; i < DV / 64; ++i)
+                tma_load_4d(sb + C::OFF_Y2 + r2.s * C::Y2_BYTES + i * C::Y_CHUNK, tmY2, f2, i * 64, y0, hy, it.b);
+            r2.next();
+            ++issued2;
+            if (++y == it.n_y) y = 0, ++hy;
         }
-    } else if (warp == 1) {
-        // ------------------------------------------------- MMA issuer --
-        if (n > 0) {
-            constexpr uint32_t id_st = idesc_bf16_f32(128, BN, false, false);
-            auto wait = [&](uint32_t br, uint32_t parity) { return mbar_wait_warp(br, parity, abort_flag, &g_bwd_err); };
-            // 128 x BN product over D columns of a resident operand and a
-            // tile, both K-major.
-            auto product = [&](uint32_t d, auto in_tmem, uint32_t xt_, uint32_t xs, uint32_t ys, int D) {
-                const uint64_t x = sdesc_sw128(xs, 16, 1024), yd = sdesc_sw128(ys, 16, 1024);
+        return true;
+    }
+    // After an abort: lets the copies already in flight land.
+    FA_DEV void drain(const BwdCta &c, int bars) const {
+        for (int i = max(0, issued1 - C::NST1); i < issued1; ++i)
+            mbar_wait_drain(c.bar(bars + C::FULL1 + i % C::NST1), (uint32_t)(i / C::NST1) & 1u);
+        for (int i = max(0, issued2 - C::NST2); i < issued2; ++i)
+            mbar_wait_drain(c.bar(bars + C::FULL2 + i % C::NST2), (uint32_t)(i / C::NST2) & 1u);
+        for (int i = max(0, walks - 1); i < walks; ++i) {
+            mbar_wait_drain(c.bar(bars + B_X1FULL), (uint32_t)i & 1u);
+            mbar_wait_drain(c.bar(bars + B_X2FULL), (uint32_t)i & 1u);
+        }
+        if (x1_pending) mbar_wait_drain(c.bar(bars + B_X1FULL), (uint32_t)walks & 1u);
+    }
+};
+
+// ---- warp 1: MMA issuer (the whole warp, one elected lane issues) ------------
+template <int DK, int DV, bool KV, class C>
+struct BwdIssuer {
+    Ring<C::NST1> s1, a1;  // Y1 stages of the next S and of the next dS product
+    Ring<C::NST2> s2, a2;  // Y2 stages of the next T and of the next P product
+    Ring<C::NST1> e1;      // Y1 stage of the tile whose T comes next (its rows' D)
+    uint32_t walks = 0, tiles_s = 0, tiles_t = 0, tiles = 0;
+
+    // 128 x BN product over D columns of a resident operand and a tile, both
+    // K-major.
+    template <int D>
+    FA_DEV static void product(uint32_t d, uint32_t xs, uint32_t ys) {
+        constexpr uint32_t id = idesc_bf16_f32(128, C::BN, false, false);
+        const uint64_t x = sdesc_sw128(xs, 16, 1024), y = sdesc_sw128(ys, 16, 1024);
 #pragma unroll
-                for (int c = 0; c < D / 64; ++c) {
-                    const uint64_t yc = yd + (uint64_t)((c * C::Y_CHUNK) >> 4);
-                    if constexpr (decltype(in_tmem)::value)
-                        mma_ts4_warp<8, 2>(d, xt_ + c * 32, yc, id_st, c > 0);
-                    else
-                        mma_ss4_warp<2, 4, 6>(d, x + (uint64_t)((c * C::X_CHUNK) >> 4), yc, id_st, c > 0);
-                }
-            };
-            // Accumulator += (P or dS) Y over the tile's BN rows.
-            auto accumulate = [&](uint32_t d, uint32_t pa, uint32_t ys, uint32_t id, bool first) {
-                const uint64_t yd = sdesc_sw128(ys, C::Y_CHUNK, 1024);
-                mma_ts4at_warp<8, C::WG_COLS, C::WG_COLS + 8, 128>(d, pa, yd, id, !first);
-                if constexpr (BN == 128)
-                    mma_ts4at_warp<8, C::WG_COLS, C::WG_COLS + 8, 128>(d, pa + 2 * C::WG_COLS, yd + 512, id, 1);
-                else
-                    mma_ts2_warp<8, 128>(d, pa + 2 * C::WG_COLS, yd + 512, id, 1);
-            };
-            // The step that adds -LSE to S, or -D to T (Y1's stage holds both).
-            auto extra = [&](uint32_t d, uint32_t off, int t) {
-                if (C::EXT)
-                    mma_ss_warp(d, sdesc_plain(sbase + off, 2048, 128),
-                                sdesc_plain(sbase + C::OFF_ROW + (t % NST1) * C::ROW_BYTES, BN * 16, 128), id_st, 1);
-            };
-            auto issue_s = [&](int t) -> bool {
-                const int s = t % NST1;
-                if (!wait(full1(s), (uint32_t)(t / NST1) & 1u)) return false;
-                if (!C::ALIAS && t > 0 && !wait(bar(B_SREAD), (uint32_t)(t - 1) & 1u)) return false;
+        for (int c = 0; c < D / 64; ++c)
+            mma_ss4_warp<2, 4, 6>(d, x + (uint64_t)((c * C::X_CHUNK) >> 4), y + (uint64_t)((c * C::Y_CHUNK) >> 4), id, c > 0);
+    }
+    // Accumulator += (P or dS) Y over the tile's BN rows.
+    template <int D>
+    FA_DEV static void accumulate(uint32_t d, uint32_t pa, uint32_t ys, bool first) {
+        constexpr uint32_t id = idesc_bf16_f32(128, D, false, true);
+        const uint64_t y = sdesc_sw128(ys, C::Y_CHUNK, 1024);
+        mma_ts4at_warp<8, C::WG_COLS, C::WG_COLS + 8, 128>(d, pa, y, id, !first);
+        if constexpr (C::BN == 128)
+            mma_ts4at_warp<8, C::WG_COLS, C::WG_COLS + 8, 128>(d, pa + 2 * C::WG_COLS, y + 512, id, 1);
+        else
+            mma_ts2_warp<8, 128>(d, pa + 2 * C::WG_COLS, y + 512, id, 1);
+    }
+    // The step that adds -LSE to S (off 0) or -D to T (off EXT_A).
+    FA_DEV static void extra(const BwdCta &c, uint32_t d, uint32_t off, int stage) {
+        if (C::EXT)
+            mma_ss_warp(d, sdesc_plain(c.sbase + off, 2048, 128),
+                        sdesc_plain(c.sbase + C::OFF_ROW + stage * C::ROW_BYTES, C::BN * 16, 128),
+                        idesc_bf16_f32(128, C::BN, false, false), 1);
+    }
+    FA_DEV bool issue_s(const BwdCta &c, int bars, bool first, bool last) {
+        if (first && !c.wait(bars + B_X1FULL, walks & 1u)) return false;
+        if (!c.wait(bars + C::FULL1 + s1.s, s1.ph)) return false;
+        if (!C::ALIAS && tiles_s > 0 && !c.wait(bars + B_SREAD, (tiles_s - 1) & 1u)) return false;
+        tc_fence_after();
+        product<DK>(c.tmem + C::T_S, c.sbase + C::OFF_X1, c.sbase + C::OFF_Y1 + s1.s * C::Y1_BYTES);
+        extra(c, c.tmem + C::T_S, 0, s1.s);
+        mma_commit_warp(c.bar(bars + B_SFULL));
+        if (last) mma_commit_warp(c.bar(bars + B_X1FREE));
+        s1.next();
+        ++tiles_s;
+        return true;
+    }
+    FA_DEV bool issue_t(const BwdCta &c, int bars, bool first, bool last) {
+        if (first && !c.wait(bars + B_X2FULL, walks & 1u)) return false;
+        if (!c.wait(bars + C::FULL2 + s2.s, s2.ph)) return false;
+        if (!C::ALIAS && tiles_t > 0 && !c.wait(bars + B_TREAD, (tiles_t - 1) & 1u)) return false;
+        tc_fence_after();
+        product<DV>(c.tmem + C::T_T, c.sbase + C::OFF_X2, c.sbase + C::OFF_Y2 + s2.s * C::Y2_BYTES);
+        extra(c, c.tmem + C::T_T, C::EXT_A, e1.s);
+        mma_commit_warp(c.bar(bars + B_TFULL));
+        if (!KV) mma_commit_warp(c.bar(bars + C::EMPTY2 + s2.s));
+        if (last) mma_commit_warp(c.bar(bars + B_X2FREE));
+        s2.next();
+        e1.next();
+        ++tiles_t;
+        return true;
+    }
+    FA_DEV bool item(const BwdCta &c, int n, int bars, int done) {
+        if (n == 0) return true;
+        if (!issue_s(c, bars, true, n == 1) || !issue_t(c, bars, true, n == 1)) return false;
+        ++walks;
+        for (int t = 0; t < n; ++t) {
+            const bool more = t + 1 < n, last = t + 2 == n;
+            if (!C::ALIAS && more && !issue_s(c, bars, false, last)) return false;
+            if (KV) {
+                if (!c.wait(bars + B_PREADY, tiles & 1u)) return false;
                 tc_fence_after();
-                product(tmem + C::T_S, std::integral_constant<bool, C::X1_TMEM>{}, tmem + C::T_X, sX1, sbase + C::y1(s), DK);
-                extra(tmem + C::T_S, 0, t);
-                mma_commit_warp(bar(B_SFULL));
-                return true;
-            };
-            auto issue_t = [&](int t) -> bool {
-                const int s = t % NST2;
-                if (!wait(full2(s), (uint32_t)(t / NST2) & 1u)) return false;
-                if (!C::ALIAS && t > 0 && !wait(bar(B_TREAD), (uint32_t)(t - 1) & 1u)) return false;
-                tc_fence_after();
-                product(tmem + C::T_T, std::integral_constant<bool, C::X2_TMEM>{}, tmem + C::T_X2, sX2, sY2 + s * C::Y2_BYTES, DV);
-                extra(tmem + C::T_T, C::EXT_A, t);
-                mma_commit_warp(bar(B_TFULL));
-                if (!KV) mma_commit_warp(empty2(s));
-                return true;
-            };
-            bool ok = wait(bar(B_XFULL), 0);
-            if (ok && C::X_TMEM) ok = wait(bar(B_XTMEM), 0);
-            ok = ok && issue_s(0) && issue_t(0);
-            for (int t = 0; ok && t < n; ++t) {
-                const int s1 = t % NST1, s2 = t % NST2;
-                const bool more = t + 1 < n;
-                if (!C::ALIAS && more && !issue_s(t + 1)) break;
-                if (KV) {
-                    if (!wait(bar(B_PREADY), (uint32_t)t & 1u)) break;
-                    tc_fence_after();
-                    accumulate(tmem + C::T_A2, tmem + C::T_P, sY2 + s2 * C::Y2_BYTES,
-                               idesc_bf16_f32(128, DV, false, true), t == 0);
-                    mma_commit_warp(empty2(s2));
-                }
-                // In place of P and dS: behind the products that read them.
-                if (C::ALIAS && more && !issue_s(t + 1)) break;
-                if (!C::ALIAS && more && !issue_t(t + 1)) break;
-                if (!wait(bar(B_DSREADY), (uint32_t)t & 1u)) break;
-                tc_fence_after();
-                accumulate(tmem + C::T_A1, tmem + C::T_D, sbase + C::y1(s1), idesc_bf16_f32(128, DK, false, true),
-                           t == 0);
-                mma_commit_warp(empty1(s1));
-                if (C::ALIAS && more && !issue_t(t + 1)) break;
+                accumulate<DV>(c.tmem + C::T_A2, c.tmem + C::T_P, c.sbase + C::OFF_Y2 + a2.s * C::Y2_BYTES, t == 0);
+                mma_commit_warp(c.bar(bars + C::EMPTY2 + a2.s));
+                a2.next();
             }
-            // Nothing of ours may still run on the tensor core once TMEM is
-            // read out or freed.
-            mma_commit_warp(bar(B_DONE));
-            mbar_wait_drain(bar(B_DONE), 0);
+            // In place of P and dS: behind the products that read them.
+            if (C::ALIAS && more && !issue_s(c, bars, false, last)) return false;
+            if (!C::ALIAS && more && !issue_t(c, bars, false, last)) return false;
+            if (!c.wait(bars + B_DSREADY, tiles & 1u)) return false;
+            tc_fence_after();
+            accumulate<DK>(c.tmem + C::T_A1, c.tmem + C::T_D, c.sbase + C::OFF_Y1 + a1.s * C::Y1_BYTES, t == 0);
+            mma_commit_warp(c.bar(bars + C::EMPTY1 + a1.s));
+            a1.next();
+            if (C::ALIAS && more && !issue_t(c, bars, false, last)) return false;
+            ++tiles;
         }
+        mma_commit_warp(c.bar(done));
+        return true;
+    }
+};
+
+// ---- warps 4 ..: P, dS, epilogue -------------------------------------------------
+
+// Four 16-byte units a lane (unit u of its own row) to: lane l of each group
+// of four holds unit l % 4 of the group's rows 0 .. 3, so that four lanes write
+// 64 contiguous bytes of one row.
+FA_DEV void transpose4(uint4 (&u)[4], int lane) {
+    const auto swap = [&](uint4 &x, uint4 &y, int d, bool up) {
+        // the lane with the bit clear gives y and keeps x, the other the reverse
+        const uint4 give = up ? x : y;
+        const uint4 got = make_uint4(__shfl_xor_sync(0xffffffffu, give.x, d), __shfl_xor_sync(0xffffffffu, give.y, d),
+                                     __shfl_xor_sync(0xffffffffu, give.z, d), __shfl_xor_sync(0xffffffffu, give.w, d));
+        if (up)
+            x = got;
+        else
+            y = got;
+    };
+    const bool b0 = lane & 1, b1 = lane & 2;
+    swap(u[0], u[1], 1, b0);
+    swap(u[2], u[3], 1, b0);
+    swap(u[0], u[2], 2, b1);
+    swap(u[1], u[3], 2, b1);
+}
+
+// 32 columns (fp32 bits in r, times f) of 32 rows of a gradient: this lane's
+// row is row0 + lane, rows at or past S are not stored.
+FA_DEV void store_rows(const BwdGrad &g, int bf16, int b, int h, int row0, int S, int col, const uint32_t (&r)[32], float f,
+                       int lane) {
+    const int q = lane & 3, first = row0 + (lane & ~3);
+    char *base = g.p + ((int64_t)b * g.sb + (int64_t)h * g.sh) * (bf16 ? 2 : 4);
+    const int units = bf16 ? 1 : 2;  // of 64 bytes
+    for (int v = 0; v < units; ++v) {
+        uint4 u[4];
+        if (bf16) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                u[i] = make_uint4(pack_bf16x2(__uint_as_float(r[8 * i]) * f, __uint_as_float(r[8 * i + 1]) * f),
+                                  pack_bf16x2(__uint_as_float(r[8 * i + 2]) * f, __uint_as_float(r[8 * i + 3]) * f),
+                                  pack_bf16x2(__uint_as_float(r[8 * i + 4]) * f, __uint_as_float(r[8 * i + 5]) * f),
+                                  pack_bf16x2(__uint_as_float(r[8 * i + 6]) * f, __uint_as_float(r[8 * i + 7]) * f));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    w[j] = __float_as_uint(__uint_as_float(v ? r[16 + 4 * i + j] : r[4 * i + j]) * f);
+                u[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+        transpose4(u, lane);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (first + i < S)
+                *reinterpret_cast<uint4 *>(base + ((int64_t)(first + i) * g.ss + col) * (bf16 ? 2 : 4) + 64 * v + 16 * q) =
+                    u[i];
+    }
+}
+
+template <int DK, int DV, bool KV, bool MODS, class C>
+struct BwdWorker {
+    Ring<C::NST1> r1, p1;  // Y1 stage of this tile, of the tile before
+    Ring<C::NST2> p2;      // Y2 stage of the tile before
+    uint32_t tiles = 0;
+
+    FA_DEV static void arrive(const BwdCta &c, int i, int lane) {
+        tc_fence_before();
         __syncwarp();
-    } else if (warp >= 4) {
-        // --------------------------------------------- P, dS, epilogue --
+        if (lane == 0) mbar_arrive(c.bar(i));
+    }
+
+    FA_DEV bool item(const BwdCta &c, const BwdArgs &a, const BwdItem &it, int bars, int done, uint32_t &dones) {
+        constexpr int BN = C::BN;
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
         const int wg = (warp >> 2) - 1;           // columns 32 wg .. 32 wg + 31 of each tile
         const int row = (warp & 3) * 32 + lane;   // resident row: key or query
-        const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t tl = c.tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t tS = tl + C::T_S + wg * 32, tT = tl + C::T_T + wg * 32;
         const uint32_t tP = tl + C::T_P + wg * C::WG_COLS, tD = tl + C::T_D + wg * C::WG_COLS;
-        const int xr = x0 + row;
-        auto wait = [&](uint32_t br, uint32_t parity) { return mbar_wait_warp(br, parity, abort_flag, &g_bwd_err); };
-        auto arrive = [&](int i) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(i));
-        };
+        const int x0 = it.x0, xr = x0 + row;
+        const int shift = a.Sk - a.Sq;
         const bool capped = MODS && a.mods.softcap != 0.f;
         const bool masked = MODS && a.mods.mask != nullptr;
         float row_nlse = 0.f, row_ndelta = 0.f;
         if (!KV) {  // rows past Sq are padded in the workspace
-            const int64_t r = ((int64_t)b * a.Hq + h) * a.pitch + xr;
+            const int64_t r = ((int64_t)it.b * a.Hq + it.h) * a.pitch + xr;
             row_nlse = __ldg(a.nlse2 + r);
             row_ndelta = __ldg(a.ndelta + r);
         }
@@ -363,29 +453,12 @@ bwd_tile_kernel(const __grid_constant__ CUtensorMap tmX1, const __grid_constant_
         const int lim_hi = a.causal ? min(a.Sk, xr + shift + 1) : a.Sk;
         const int lim_lo = a.causal ? xr - shift : 0;
         const uint64_t sc2 = f2_pack(a.scale_log2, a.scale_log2);
-        bool ok = true;
-        if (C::X_TMEM && n > 0) {
-            ok = wait(bar(B_XFULL), 0);
-            if (ok) {
-                constexpr int N1 = C::X1_TMEM ? DK / 64 : 0, NC = N1 + (C::X2_TMEM ? DV / 64 : 0);
-#pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    if (c % (BN / 32) == wg)
-                        chunk_to_tmem(c < N1 ? smem + C::OFF_X1 + c * C::X_CHUNK : smem + C::OFF_X2 + (c - N1) * C::X_CHUNK, row,
-                                      tl + (uint32_t)(C::T_X + c * 32));
-                }
-                tmem_wait_st();
-                arrive(B_XTMEM);
-            }
-        }
-        int y = 0, hq = KV ? h * group : h;
-        for (int t = 0; ok && t < n; ++t) {
-            ok = false;
-            const int s1 = t % NST1;
-            const int y0 = (y_first + y) * BN + wg * 32;  // first column: query or key
-            const float *sl = reinterpret_cast<const float *>(smem + C::OFF_ROW + s1 * C::ROW_BYTES) + wg * 32;
-            if (KV && MODS && !wait(full1(s1), (uint32_t)(t / NST1) & 1u)) break;
-            if (!wait(bar(B_SFULL), (uint32_t)t & 1u)) break;
+        int y = 0, hq = KV ? it.h * (a.Hq / a.Hkv) : it.h;
+        for (int t = 0; t < it.n; ++t) {
+            const int y0 = (it.y_first + y) * BN + wg * 32;  // first column: query or key
+            const float *sl = reinterpret_cast<const float *>(c.smem + C::OFF_ROW + r1.s * C::ROW_BYTES) + wg * 32;
+            if (KV && MODS && !c.wait(bars + C::FULL1 + r1.s, r1.ph)) return false;
+            if (!c.wait(bars + B_SFULL, tiles & 1u)) return false;
             tc_fence_after();
             float x[32];
             {
@@ -396,7 +469,7 @@ bwd_tile_kernel(const __grid_constant__ CUtensorMap tmX1, const __grid_constant_
 #pragma unroll
                 for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(r[i]);
             }
-            if (!C::ALIAS) arrive(B_SREAD);
+            if (!C::ALIAS) arrive(c, bars + B_SREAD, lane);
             float cap[MODS ? 32 : 1];  // ds/dz under a softcap
             if constexpr (MODS) {
                 const float slope = alibi_slope(a.mods, hq) * kLog2e;
@@ -416,7 +489,7 @@ bwd_tile_kernel(const __grid_constant__ CUtensorMap tmX1, const __grid_constant_
                 if (masked) {
                     // Rows and keys past the end read the last one's values:
                     // their P is 0, or their results are not stored.
-                    const __half *m = a.mods.mask + (int64_t)b * a.mods.m_sb + (int64_t)hq * a.mods.m_sh;
+                    const __half *m = a.mods.mask + (int64_t)it.b * a.mods.m_sb + (int64_t)hq * a.mods.m_sh;
                     if (KV) {
                         m += min(xr, a.Sk - 1);
 #pragma unroll
@@ -481,23 +554,26 @@ bwd_tile_kernel(const __grid_constant__ CUtensorMap tmX1, const __grid_constant_
             }
             if (KV) {
                 // With its own columns: the product over the P before is done.
-                if (!C::ALIAS && t > 0 && !wait(empty2((t - 1) % NST2), (uint32_t)((t - 1) / NST2) & 1u)) break;
+                if (!C::ALIAS && tiles > 0) {
+                    if (!c.wait(bars + C::EMPTY2 + p2.s, p2.ph)) return false;
+                    p2.next();
+                }
                 tmem_st16(tP, pk);
                 tmem_wait_st();
-                arrive(B_PREADY);
+                arrive(c, bars + B_PREADY, lane);
             }
             if (MODS && capped) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) x[i] *= cap[i];
             }
             // dS
-            if (!wait(bar(B_TFULL), (uint32_t)t & 1u)) break;
+            if (!c.wait(bars + B_TFULL, tiles & 1u)) return false;
             tc_fence_after();
             uint32_t r[32];
             tmem_ld32(tT, r);
             tmem_wait_ld();
             reg_fence(r);
-            if (!C::ALIAS) arrive(B_TREAD);
+            if (!C::ALIAS) arrive(c, bars + B_TREAD, lane);
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
                 uint64_t nd[2];
@@ -519,51 +595,176 @@ bwd_tile_kernel(const __grid_constant__ CUtensorMap tmX1, const __grid_constant_
                     pk[k / 2] = pack_bf16x2(d0, d1);
                 }
             }
-            if (!C::ALIAS && t > 0 && !wait(empty1((t - 1) % NST1), (uint32_t)((t - 1) / NST1) & 1u)) break;
+            if (!C::ALIAS && tiles > 0) {
+                if (!c.wait(bars + C::EMPTY1 + p1.s, p1.ph)) return false;
+                p1.next();
+            }
             tmem_st16(tD, pk);
             tmem_wait_st();
-            arrive(B_DSREADY);
-            if (++y == n_y) y = 0, ++hq;
-            ok = true;
+            arrive(c, bars + B_DSREADY, lane);
+            r1.next();
+            ++tiles;
+            if (++y == it.n_y) y = 0, ++hq;
         }
-        bool have = ok && n > 0;
-        if (have) {
-            have = wait(bar(B_DONE), 0);
+        if (it.n > 0) {
+            if (!c.wait(done, dones & 1u)) return false;
+            ++dones;
             tc_fence_after();
         }
-        // 32 accumulator columns at a time, dealt to the warpgroups.
-        const bool store = xr < (KV ? a.Sk : a.Sq);
-        const int64_t off1 = (int64_t)b * a.g1_sb + (int64_t)h * a.g1_sh + (int64_t)xr * a.g1_ss;
-        const int64_t off2 = (int64_t)b * a.g2_sb + (int64_t)h * a.g2_sh + (int64_t)xr * a.g2_ss;
-        for (int c = wg * 32; c < C::ACC; c += BN) {
-            const bool second = c >= DK;
+        // 32 accumulator columns at a time, dealt to the warpgroups.  The next
+        // item's products into the accumulators wait for this warp's next P
+        // and dS, so they cannot come before these loads.
+        const int row0 = x0 + (warp & 3) * 32, S = KV ? a.Sk : a.Sq;
+        for (int col = wg * 32; col < C::ACC; col += BN) {
+            const bool second = col >= DK;
             uint32_t r[32];
-            if (have) {
-                tmem_ld32(tl + (uint32_t)(C::T_A1 + c), r);
+            if (it.n > 0) {
+                tmem_ld32(tl + (uint32_t)(C::T_A1 + col), r);
                 tmem_wait_ld();
                 reg_fence(r);
             } else {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) r[i] = 0u;
             }
-            if (!store) continue;
-            const float f = second ? 1.f : a.scale;
-            const int64_t at = second ? off2 + c - DK : off1 + c;
-            char *base = second ? a.g2 : a.g1;
-            if (a.g_bf16) {
-                uint4 *dst = reinterpret_cast<uint4 *>(base + 2 * at);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    dst[i] = make_uint4(pack_bf16x2(__uint_as_float(r[8 * i]) * f, __uint_as_float(r[8 * i + 1]) * f),
-                                        pack_bf16x2(__uint_as_float(r[8 * i + 2]) * f, __uint_as_float(r[8 * i + 3]) * f),
-                                        pack_bf16x2(__uint_as_float(r[8 * i + 4]) * f, __uint_as_float(r[8 * i + 5]) * f),
-                                        pack_bf16x2(__uint_as_float(r[8 * i + 6]) * f, __uint_as_float(r[8 * i + 7]) * f));
+            store_rows(KV ? (second ? a.gv : a.gk) : a.gq, a.g_bf16, it.b, it.h, row0, S, second ? col - DK : col, r,
+                       second ? 1.f : a.scale, lane);
+        }
+        return true;
+    }
+};
+
+// Persistent: one CTA an SM takes items from a counter until none is left.
+template <int DK, int DV, bool MODS>
+__global__ void __launch_bounds__(BwdKernel<DK, DV, MODS>::THREADS, 1)
+bwd_tile_kernel(const __grid_constant__ CUtensorMap tmQx, const __grid_constant__ CUtensorMap tmKx,
+                const __grid_constant__ CUtensorMap tmVx, const __grid_constant__ CUtensorMap tmDOx,
+                const __grid_constant__ CUtensorMap tmQy, const __grid_constant__ CUtensorMap tmKy,
+                const __grid_constant__ CUtensorMap tmVy, const __grid_constant__ CUtensorMap tmDOy, const BwdArgs a) {
+    using K = BwdKernel<DK, DV, MODS>;
+    using CK = typename K::CK;
+    using CQ = typename K::CQ;
+    constexpr int BN = CK::BN, WARPS = CK::WARPS;
+    extern __shared__ uint8_t smem_raw[];
+    BwdCta c;
+    c.smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    c.sbase = smem_u32(c.smem);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(c.smem + K::OFF_BAR);
+    c.bar0 = smem_u32(bars);
+    volatile int *slot = reinterpret_cast<volatile int *>(bars + K::BARS);  // two items
+    uint32_t *tmem_holder = const_cast<uint32_t *>(reinterpret_cast<volatile uint32_t *>(slot + 2));
+    c.abort_flag = slot + 3;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < K::BARS; ++i) {
+            int count = 1;
+            if (i == 2 || i == 3) count = 1 + WARPS;  // an item is free once the issuer and the workers have it
+            if (i == K::BAR_MOVED) count = WARPS;
+            const int j = i >= K::BAR_Q ? i - K::BAR_Q : i - K::BAR_KV;
+            if (i >= K::BAR_KV && j >= B_SREAD && j <= B_DSREADY) count = WARPS;
+            mbar_init(c.bar(i), count);
+        }
+        *c.abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (CK::EXT) {
+        // A side of the extra step: row = 1 in columns 0 .. 2 for S (the three
+        // pieces of the LSE), 3 .. 5 for T (those of D); the second half of
+        // its 16 columns, on both sides, is zeros.
+        uint4 *e = reinterpret_cast<uint4 *>(c.smem);
+        for (int i = threadIdx.x; i < 2 * CK::EXT_A / 16; i += K::THREADS)
+            e[i] = (i & 128) ? make_uint4(0, 0, 0, 0)
+                   : i < 256 ? make_uint4(0x3f803f80u, 0x3f80u, 0, 0)
+                             : make_uint4(0, 0x3f800000u, 0x3f803f80u, 0);
+        for (int i = threadIdx.x; i < CK::NST1 * BN; i += K::THREADS)
+            reinterpret_cast<uint4 *>(c.smem + CK::OFF_ROW + (i / BN) * CK::ROW_BYTES)[BN + i % BN] = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_holder), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    c.tmem = *tmem_holder;
+
+    // Item k of this CTA, or -1: waits until the producer has put it there.
+    auto take = [&](int k) -> int {
+        if (!c.wait(k & 1, (uint32_t)(k >> 1) & 1u)) return -1;
+        const int i = slot[k & 1];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(c.bar(2 + (k & 1)));
+        return i < a.items ? i : -1;
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            if (a.Sq > 0 && a.Sk > 0) {  // an empty side has no maps
+                prefetch_tmap(&tmQx), prefetch_tmap(&tmKx), prefetch_tmap(&tmVx), prefetch_tmap(&tmDOx);
+                prefetch_tmap(&tmQy), prefetch_tmap(&tmKy), prefetch_tmap(&tmVy), prefetch_tmap(&tmDOy);
+            }
+            BwdProducer<CK> pk;
+            BwdProducer<CQ> pq;
+            int ahead = atomicAdd(a.next, 1);
+            uint32_t kv_walks = 0;
+            bool moved = false;
+            for (int k = 0;; ++k) {
+                const int i = ahead;
+                if (!c.wait1(2 + (k & 1), ((uint32_t)(k >> 1) & 1u) ^ 1u)) break;
+                slot[k & 1] = i;
+                mbar_arrive(c.bar(k & 1));
+                if (i >= a.items) break;
+                ahead = atomicAdd(a.next, 1);  // its latency passes under this item
+                if (i < a.kv_items) {
+                    const BwdItem it = bwd_item<true, BN>(a, i);
+                    kv_walks += it.n > 0;
+                    if (!pk.template item<DK, DV, true>(c, a, it, K::BAR_KV, &tmKx, &tmVx, &tmQy, &tmDOy)) break;
+                } else {
+                    // dQ lays shared memory out anew: the last dK / dV item's
+                    // products must be done with it.
+                    if (!moved && kv_walks > 0 && !c.wait1(K::BAR_DONE, (kv_walks - 1) & 1u)) break;
+                    moved = true;
+                    const BwdItem it = bwd_item<false, BN>(a, i);
+                    if (!pq.template item<DK, DV, false>(c, a, it, K::BAR_Q, &tmQx, &tmDOx, &tmKy, &tmVy)) break;
+                }
+            }
+            if (*c.abort_flag) {
+                pk.drain(c, K::BAR_KV);
+                pq.drain(c, K::BAR_Q);
+            }
+        }
+    } else if (warp == 1) {
+        BwdIssuer<DK, DV, true, CK> ik;
+        BwdIssuer<DK, DV, false, CQ> iq;
+        for (int k = 0, i; (i = take(k)) >= 0; ++k) {
+            if (i < a.kv_items) {
+                if (!ik.item(c, bwd_item<true, BN>(a, i).n, K::BAR_KV, K::BAR_DONE)) break;
             } else {
-                float4 *dst = reinterpret_cast<float4 *>(base + 4 * at);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    dst[i] = make_float4(__uint_as_float(r[4 * i]) * f, __uint_as_float(r[4 * i + 1]) * f,
-                                         __uint_as_float(r[4 * i + 2]) * f, __uint_as_float(r[4 * i + 3]) * f);
+                if (!iq.item(c, bwd_item<false, BN>(a, i).n, K::BAR_Q, K::BAR_DONE)) break;
+            }
+        }
+        // Nothing of ours may still run on the tensor core once TMEM is freed.
+        mma_commit_warp(c.bar(K::BAR_END));
+        mbar_wait_drain(c.bar(K::BAR_END), 0);
+        __syncwarp();
+    } else if (warp >= 4) {
+        BwdWorker<DK, DV, true, MODS, CK> wk;
+        BwdWorker<DK, DV, false, MODS, CQ> wq;
+        uint32_t dones = 0;
+        bool kv = false;
+        for (int k = 0, i; (i = take(k)) >= 0; ++k) {
+            if (i < a.kv_items) {
+                kv = true;
+                if (!wk.item(c, a, bwd_item<true, BN>(a, i), K::BAR_KV, K::BAR_DONE, dones)) break;
+            } else {
+                if (kv) {
+                    // dQ's dS may lie where dK and dV were: every warp must have read them.
+                    wq.arrive(c, K::BAR_MOVED, lane);
+                    if (!c.wait(K::BAR_MOVED, 0)) break;
+                    kv = false;
+                }
+                if (!wq.item(c, a, bwd_item<false, BN>(a, i), K::BAR_Q, K::BAR_DONE, dones)) break;
             }
         }
     }
@@ -572,7 +773,7 @@ bwd_tile_kernel(const __grid_constant__ CUtensorMap tmX1, const __grid_constant_
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, C::TMEM_COLS);
+        tmem_dealloc(c.tmem, 512);
     }
 }
 
@@ -586,6 +787,7 @@ struct PrepArgs {
     int64_t pitch, rows;  // rows = B * Hq * pitch
     float *nlse2, *ndelta;
     uint4 *ext;  // NULL: not wanted
+    int *next;   // set to 0
     float inv_scale;
 };
 
@@ -602,6 +804,7 @@ FA_DEV void split3(float v, uint16_t (&p)[3]) {
 template <int DV>
 __global__ void __launch_bounds__(256) bwd_prep_kernel(const PrepArgs a) {
     constexpr int LPR = DV / 8;  // lanes of a row
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.next = 0;
     const int64_t r = (int64_t)blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
     const int l = threadIdx.x % LPR;
     const int64_t bh = r / a.pitch;
@@ -676,54 +879,38 @@ __global__ void __launch_bounds__(512) bwd_sink_kernel(const float *nlse2, const
     }
 }
 
-template <int DK, int DV, bool KV, bool MODS>
-cudaError_t launch_tiles(const BwdLaunch &L, BwdArgs a, cudaStream_t stream) {
-    using C = BwdCfg<DK, DV, KV, MODS>;
-    auto kern = bwd_tile_kernel<DK, DV, KV, MODS>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
-    if (e != cudaSuccess) return e;
-    a.outer = ((KV ? L.Sk : L.Sq) + 127) / 128;
-    if (KV) {
-        a.g1 = static_cast<char *>(L.gk), a.g1_sb = L.gk_sb, a.g1_sh = L.gk_sh, a.g1_ss = L.gk_ss;
-        a.g2 = static_cast<char *>(L.gv), a.g2_sb = L.gv_sb, a.g2_sh = L.gv_sh, a.g2_ss = L.gv_ss;
-    } else {
-        a.g1 = static_cast<char *>(L.gq), a.g1_sb = L.gq_sb, a.g1_sh = L.gq_sh, a.g1_ss = L.gq_ss;
-    }
-    const unsigned grid = (unsigned)(L.B * (KV ? L.Hkv : L.Hq)) * (unsigned)a.outer;
-    if (grid == 0) return cudaSuccess;
-    if (KV)
-        kern<<<grid, C::THREADS, C::SMEM_BYTES, stream>>>(L.tmKx, L.tmVx, L.tmQy, L.tmDOy, a);
-    else
-        kern<<<grid, C::THREADS, C::SMEM_BYTES, stream>>>(L.tmQx, L.tmDOx, L.tmKy, L.tmVy, a);
-    return cudaGetLastError();
-}
-
 template <int DK, int DV, bool MODS>
-cudaError_t launch_pair(const BwdLaunch &L, const BwdArgs &a, cudaStream_t stream) {
-    cudaError_t e = launch_tiles<DK, DV, true, MODS>(L, a, stream);
-    if (e == cudaSuccess) e = launch_tiles<DK, DV, false, MODS>(L, a, stream);
-    return e;
+cudaError_t launch_tiles(const BwdLaunch &L, const BwdArgs &a, int num_sms, cudaStream_t stream) {
+    using K = BwdKernel<DK, DV, MODS>;
+    auto kern = bwd_tile_kernel<DK, DV, MODS>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, K::SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    const int grid = a.items < num_sms ? a.items : num_sms;
+    if (grid == 0) return cudaSuccess;
+    kern<<<grid, K::THREADS, K::SMEM_BYTES, stream>>>(L.tmQx, L.tmKx, L.tmVx, L.tmDOx, L.tmQy, L.tmKy, L.tmVy, L.tmDOy, a);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_bwd(const BwdLaunch &L, cudaStream_t stream) {
+cudaError_t launch_bwd(const BwdLaunch &L, int num_sms, cudaStream_t stream) {
     const int64_t pitch = bwd_pitch(L.Sq);
-    if (L.Sq > 0 && L.B > 0) {
+    {
         PrepArgs p;
         p.o = L.o, p.dout = static_cast<const __nv_bfloat16 *>(L.dout), p.lse = L.lse, p.dlse = L.dlse;
         p.o_sb = L.o_sb, p.o_sh = L.o_sh, p.o_ss = L.o_ss;
         p.do_sb = L.do_sb, p.do_sh = L.do_sh, p.do_ss = L.do_ss;
         p.Hq = L.Hq, p.Sq = L.Sq, p.o_bf16 = L.o_bf16;
-        p.pitch = pitch, p.rows = (int64_t)L.B * L.Hq * pitch;
+        p.pitch = pitch > 0 ? pitch : 1, p.rows = (int64_t)L.B * L.Hq * pitch;
         p.nlse2 = L.nlse2, p.ndelta = L.ndelta;
         p.ext = L.has_mods ? nullptr : static_cast<uint4 *>(L.ext), p.inv_scale = 1.f / L.scale;
+        p.next = L.next;
         const int per = 256 / (L.dv / 8);
         const unsigned grid = (unsigned)((p.rows + per - 1) / per);
         if (L.dv == 64)
-            bwd_prep_kernel<64><<<grid, 256, 0, stream>>>(p);
+            bwd_prep_kernel<64><<<grid > 0 ? grid : 1, 256, 0, stream>>>(p);
         else
-            bwd_prep_kernel<128><<<grid, 256, 0, stream>>>(p);
+            bwd_prep_kernel<128><<<grid > 0 ? grid : 1, 256, 0, stream>>>(p);
         cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
@@ -733,13 +920,19 @@ cudaError_t launch_bwd(const BwdLaunch &L, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
     }
     BwdArgs a = {};
-    a.Hq = L.Hq, a.Hkv = L.Hkv, a.Sq = L.Sq, a.Sk = L.Sk, a.causal = L.causal;
+    a.B = L.B, a.Hq = L.Hq, a.Hkv = L.Hkv, a.Sq = L.Sq, a.Sk = L.Sk, a.causal = L.causal;
     a.scale = L.scale, a.scale_log2 = L.scale * kLog2e;
     a.mods = L.mods;
     a.nlse2 = L.nlse2, a.ndelta = L.ndelta, a.ext = static_cast<const uint4 *>(L.ext), a.pitch = pitch;
+    a.kv_items = L.B * L.Hkv * ((L.Sk + 127) / 128);
+    a.items = a.kv_items + L.B * L.Hq * ((L.Sq + 127) / 128);
+    a.next = L.next;
+    a.gq = BwdGrad{static_cast<char *>(L.gq), L.gq_sb, L.gq_sh, L.gq_ss};
+    a.gk = BwdGrad{static_cast<char *>(L.gk), L.gk_sb, L.gk_sh, L.gk_ss};
+    a.gv = BwdGrad{static_cast<char *>(L.gv), L.gv_sb, L.gv_sh, L.gv_ss};
     a.g_bf16 = L.g_bf16;
 #define FA_BWD_PAIR(DK_, DV_) \
-    (L.has_mods ? launch_pair<DK_, DV_, true>(L, a, stream) : launch_pair<DK_, DV_, false>(L, a, stream))
+    (L.has_mods ? launch_tiles<DK_, DV_, true>(L, a, num_sms, stream) : launch_tiles<DK_, DV_, false>(L, a, num_sms, stream))
     if (L.dk == 64 && L.dv == 64) return FA_BWD_PAIR(64, 64);
     if (L.dk == 128 && L.dv == 128) return FA_BWD_PAIR(128, 128);
     if (L.dk == 192 && L.dv == 128) return FA_BWD_PAIR(192, 128);

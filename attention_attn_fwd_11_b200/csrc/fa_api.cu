@@ -1028,7 +1028,7 @@ fa_status fa_bwd_workspace_size(const fa_bwd_params *p, size_t *bytes) {
     fa_status st = check_bwd(p);
     if (st != FA_OK) return st;
     if (!bytes) return fail(FA_ERR_INVALID_ARG, "fa_bwd_workspace_size: bytes is NULL");
-    *bytes = 6 * bwd_row_bytes(p);
+    *bytes = 6 * bwd_row_bytes(p) + 256;
     return FA_OK;
 }
 
@@ -1059,8 +1059,8 @@ fa_status fa_bwd(const fa_bwd_params *p, void *stream) {
                     p->m_sh < 0 || p->m_sb < 0))
         return fail(FA_ERR_INVALID_ARG,
                     "fa_bwd: mask must be 16-byte aligned, its strides multiples of 8 elements, m_ss >= Sk");
-    const size_t each = bwd_row_bytes(p), need = 6 * each;
-    if (need > 0 && (!p->workspace || p->workspace_bytes < need || ((uintptr_t)p->workspace & 255u)))
+    const size_t each = bwd_row_bytes(p), need = 6 * each + 256;
+    if (!p->workspace || p->workspace_bytes < need || ((uintptr_t)p->workspace & 255u))
         return fail(FA_ERR_WORKSPACE, "fa_bwd: workspace needs %zu bytes, 256-byte aligned", need);
     if (!get_encoder()) return fail(FA_ERR_CUDA, "fa_bwd: cuTensorMapEncodeTiled is not available");
     fa::BwdLaunch L;
@@ -1132,7 +1132,10 @@ fa_status fa_bwd(const fa_bwd_params *p, void *stream) {
     L.nlse2 = static_cast<float *>(p->workspace);
     L.ndelta = reinterpret_cast<float *>(static_cast<char *>(p->workspace) + each);
     L.ext = static_cast<char *>(p->workspace) + 2 * each;
-    cudaError_t e = fa::launch_bwd(L, static_cast<cudaStream_t>(stream));
+    L.next = reinterpret_cast<int *>(static_cast<char *>(p->workspace) + 6 * each);
+    int sms = 0;
+    cudaError_t e = num_sms(&sms);
+    if (e == cudaSuccess) e = fa::launch_bwd(L, sms, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "fa_bwd: launch");
     return FA_OK;
 }

@@ -210,7 +210,8 @@ struct BwdLaunch {
     bool has_mods;
     float *gsinks;   // NULL: not asked for
     float *nlse2, *ndelta;  // workspace: [B * Hq, bwd_pitch(Sq)] each,
-    void *ext;              // and as many 16-byte rows
+    void *ext;              // and as many 16-byte rows,
+    int *next;              // and the counter from which CTAs take their tiles
 };
 // Rows of nlse2 and ndelta per (batch, head): Sq rounded up to whole tiles,
 // walked (128 or 96) and the resident one (128) alike.
@@ -218,7 +219,7 @@ inline int64_t bwd_pitch(int Sq) { return ((int64_t)Sq + 383) / 384 * 384; }
 // Rows of a walked tile: 128, or what TMEM holds beside 192 + 128 columns of
 // dK and dV.
 constexpr int bwd_walk(int dk) { return dk == 192 ? 96 : 128; }
-cudaError_t launch_bwd(const BwdLaunch &L, cudaStream_t stream);
+cudaError_t launch_bwd(const BwdLaunch &L, int num_sms, cudaStream_t stream);
 cudaError_t bwd_device_error(int clear, int *code);
 
 }  // namespace fa
