@@ -43,7 +43,7 @@
 #include <cuda_runtime.h>
 #include <math.h>
 
-#include <type_traits>
+#include <atomic>
 
 #include "internal.h"
 #include "score_mods.cuh"
@@ -106,9 +106,12 @@ struct BwdCfg {
     static constexpr bool ALIAS = KV && T_END + BN > TMEM_COLS;
     static constexpr int WG_COLS = ALIAS ? 32 : 16;  // from one warpgroup's P or dS to the next
     static constexpr int T_P = ALIAS ? T_S : T_END;
-    static constexpr int T_D = ALIAS ? T_T : KV ? T_END + BN / 2 : T_END + BN / 2 <= TMEM_COLS ? T_END : DK;
-    static_assert(T_END <= TMEM_COLS && T_D + (ALIAS ? BN : BN / 2) <= TMEM_COLS, "TMEM budget");
-    static_assert(T_D >= T_END || ALIAS || T_D + BN / 2 <= T_S, "dS apart from S");
+    static constexpr int T_D = ALIAS ? T_T : KV ? T_END + BN / 2 : T_END + BN <= TMEM_COLS ? T_END : DK;
+    // dQ has two dS tiles in turn: S and T of the next tile are issued before
+    // this tile's product, so the next dS would wait for all three.
+    static constexpr int D_COLS = KV ? 0 : BN / 2;  // from one dS to the next
+    static_assert(T_END <= TMEM_COLS && T_D + (ALIAS ? BN : BN / 2 + D_COLS) <= TMEM_COLS, "TMEM budget");
+    static_assert(T_D >= T_END || ALIAS || T_D + BN <= T_S, "dS apart from S");
     // Barriers of this walk (each kind of item has its own set).
     static constexpr int FULL1 = 10, EMPTY1 = FULL1 + NST1, FULL2 = EMPTY1 + NST1, EMPTY2 = FULL2 + NST2;
     static constexpr int BARS = EMPTY2 + NST2;
@@ -173,8 +176,11 @@ struct Ring {
     }
 };
 
+#ifndef FA_POLY
+#define FA_POLY 4
+#endif
 // Of every eight exponentials, this many go to the FMA pipe (exp2_poly2).
-constexpr int kPolyOf8 = 2;
+constexpr int kPolyOf8 = FA_POLY;
 
 // What every role of a CTA shares.
 struct BwdCta {
@@ -318,7 +324,8 @@ struct BwdIssuer {
     FA_DEV bool issue_t(const BwdCta &c, int bars, bool first, bool last) {
         if (first && !c.wait(bars + B_X2FULL, walks & 1u)) return false;
         if (!c.wait(bars + C::FULL2 + s2.s, s2.ph)) return false;
-        if (!C::ALIAS && tiles_t > 0 && !c.wait(bars + B_TREAD, (tiles_t - 1) & 1u)) return false;
+        // (dK / dV: behind dS's product, so the T before has been read.)
+        if (!KV && tiles_t > 0 && !c.wait(bars + B_TREAD, (tiles_t - 1) & 1u)) return false;
         tc_fence_after();
         product<DV>(c.tmem + C::T_T, c.sbase + C::OFF_X2, c.sbase + C::OFF_Y2 + s2.s * C::Y2_BYTES);
         extra(c, c.tmem + C::T_T, C::EXT_A, e1.s);
@@ -344,15 +351,16 @@ struct BwdIssuer {
                 mma_commit_warp(c.bar(bars + C::EMPTY2 + a2.s));
                 a2.next();
             }
-            // In place of P and dS: behind the products that read them.
+            // In place of P and dS, or where nothing waits for them: behind the
+            // products that read those.
             if (C::ALIAS && more && !issue_s(c, bars, false, last)) return false;
-            if (!C::ALIAS && more && !issue_t(c, bars, false, last)) return false;
+            if (!KV && more && !issue_t(c, bars, false, last)) return false;
             if (!c.wait(bars + B_DSREADY, tiles & 1u)) return false;
             tc_fence_after();
-            accumulate<DK>(c.tmem + C::T_A1, c.tmem + C::T_D, c.sbase + C::OFF_Y1 + a1.s * C::Y1_BYTES, t == 0);
+            accumulate<DK>(c.tmem + C::T_A1, c.tmem + C::T_D + (tiles & 1u) * C::D_COLS, c.sbase + C::OFF_Y1 + a1.s * C::Y1_BYTES, t == 0);
             mma_commit_warp(c.bar(bars + C::EMPTY1 + a1.s));
             a1.next();
-            if (C::ALIAS && more && !issue_t(c, bars, false, last)) return false;
+            if (KV && more && !issue_t(c, bars, false, last)) return false;
             ++tiles;
         }
         mma_commit_warp(c.bar(done));
@@ -420,7 +428,7 @@ FA_DEV void store_rows(const BwdGrad &g, int bf16, int b, int h, int row0, int S
 
 template <int DK, int DV, bool KV, bool MODS, class C>
 struct BwdWorker {
-    Ring<C::NST1> r1, p1;  // Y1 stage of this tile, of the tile before
+    Ring<C::NST1> r1, p1;  // Y1 stage of this tile, of the tile whose dS it replaces
     Ring<C::NST2> p2;      // Y2 stage of the tile before
     uint32_t tiles = 0;
 
@@ -573,7 +581,7 @@ struct BwdWorker {
             tmem_ld32(tT, r);
             tmem_wait_ld();
             reg_fence(r);
-            if (!C::ALIAS) arrive(c, bars + B_TREAD, lane);
+            if (!KV) arrive(c, bars + B_TREAD, lane);
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
                 uint64_t nd[2];
@@ -595,11 +603,12 @@ struct BwdWorker {
                     pk[k / 2] = pack_bf16x2(d0, d1);
                 }
             }
-            if (!C::ALIAS && tiles > 0) {
+            // The product over the dS that was in these columns is done.
+            if (!C::ALIAS && tiles > (KV ? 0u : 1u)) {
                 if (!c.wait(bars + C::EMPTY1 + p1.s, p1.ph)) return false;
                 p1.next();
             }
-            tmem_st16(tD, pk);
+            tmem_st16(tD + (tiles & 1u) * C::D_COLS, pk);
             tmem_wait_st();
             arrive(c, bars + B_DSREADY, lane);
             r1.next();
@@ -777,18 +786,21 @@ bwd_tile_kernel(const __grid_constant__ CUtensorMap tmQx, const __grid_constant_
     }
 }
 
-// D and base-2 LSE of every row, DV / 8 lanes a row.
+// D and LSE of every row, DV / 8 lanes a row.  A block takes kPrepRows rows of
+// one head: each thread has the loads of all its rows under way before the
+// first is used.
+constexpr int kPrepRows = 64;
 struct PrepArgs {
     const void *o;
     const __nv_bfloat16 *dout;
     const float *lse, *dlse;
     int64_t o_sb, o_sh, o_ss, do_sb, do_sh, do_ss;
     int Hq, Sq, o_bf16;
-    int64_t pitch, rows;  // rows = B * Hq * pitch
+    int blocks;  // of kPrepRows rows, for each head
     float *nlse2, *ndelta;
     uint4 *ext;  // NULL: not wanted
-    int *next;   // set to 0
     float inv_scale;
+    int *next;  // set to 0
 };
 
 // A value as three bf16 that add up to its 24 bits.
@@ -801,47 +813,74 @@ FA_DEV void split3(float v, uint16_t (&p)[3]) {
     }
 }
 
-template <int DV>
-__global__ void __launch_bounds__(256) bwd_prep_kernel(const PrepArgs a) {
-    constexpr int LPR = DV / 8;  // lanes of a row
-    if (blockIdx.x == 0 && threadIdx.x == 0) *a.next = 0;
-    const int64_t r = (int64_t)blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
-    const int l = threadIdx.x % LPR;
-    const int64_t bh = r / a.pitch;
-    const int i = (int)(r % a.pitch), b = (int)(bh / a.Hq), h = (int)(bh % a.Hq);
+FA_DEV float dot8(const uint4 &w, const float (&o)[8]) {
+    const uint32_t g[4] = {w.x, w.y, w.z, w.w};
     float d = 0.f;
-    const bool live = r < a.rows && i < a.Sq;
-    if (live) {
-        const uint4 w = *reinterpret_cast<const uint4 *>(a.dout + b * a.do_sb + h * a.do_sh + i * a.do_ss + 8 * l);
-        const uint32_t g[4] = {w.x, w.y, w.z, w.w};
-        const int64_t off = b * a.o_sb + h * a.o_sh + i * a.o_ss + 8 * l;
-        float o[8];
-        if (a.o_bf16) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.o) + off);
-            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                o[2 * j] = __uint_as_float(u[j] << 16), o[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
+    for (int j = 0; j < 4; ++j) {
+        d = fmaf(__uint_as_float(g[j] << 16), o[2 * j], d);
+        d = fmaf(__uint_as_float(g[j] & 0xffff0000u), o[2 * j + 1], d);
+    }
+    return d;
+}
+
+template <int DV, bool O_BF16>
+__global__ void __launch_bounds__(256) bwd_prep_kernel(const PrepArgs a) {
+    constexpr int LPR = DV / 8;                    // lanes of a row
+    constexpr int N = kPrepRows * LPR / 256;       // rows of a thread
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.next = 0;
+    if (a.blocks == 0) return;
+    const int bh = (int)(blockIdx.x / (unsigned)a.blocks), r0 = (int)(blockIdx.x % (unsigned)a.blocks) * kPrepRows;
+    const int b = bh / a.Hq, h = bh % a.Hq;
+    const int l = threadIdx.x % LPR, first = r0 + threadIdx.x / LPR;
+    const __nv_bfloat16 *g = a.dout + b * a.do_sb + h * a.do_sh + 8 * l;
+    const int64_t ob = b * a.o_sb + h * a.o_sh + 8 * l;
+    uint4 w[N], u[N];
+    [[maybe_unused]] uint4 v[O_BF16 ? 1 : N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const int i = min(first + k * (256 / LPR), a.Sq - 1);
+        w[k] = __ldg(reinterpret_cast<const uint4 *>(g + i * a.do_ss));
+        if constexpr (O_BF16) {
+            u[k] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.o) + ob + i * a.o_ss));
         } else {
-            const float4 *v = reinterpret_cast<const float4 *>(static_cast<const float *>(a.o) + off);
-            const float4 p = v[0], q = v[1];
-            o[0] = p.x, o[1] = p.y, o[2] = p.z, o[3] = p.w, o[4] = q.x, o[5] = q.y, o[6] = q.z, o[7] = q.w;
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            d = fmaf(__uint_as_float(g[j] << 16), o[2 * j], d);
-            d = fmaf(__uint_as_float(g[j] & 0xffff0000u), o[2 * j + 1], d);
+            const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const float *>(a.o) + ob + i * a.o_ss);
+            u[k] = __ldg(p);
+            v[k] = __ldg(p + 1);
         }
     }
+    // Lane k of a row's lanes keeps the sum of the thread's k-th row.
+    float d = 0.f;
 #pragma unroll
-    for (int k = LPR / 2; k > 0; k >>= 1) d += __shfl_xor_sync(0xffffffffu, d, k);
-    if (l == 0 && r < a.rows) {
+    for (int k = 0; k < N; ++k) {
+        float o[8];
+        if constexpr (O_BF16) {
+            const uint32_t t[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                o[2 * j] = __uint_as_float(t[j] << 16), o[2 * j + 1] = __uint_as_float(t[j] & 0xffff0000u);
+        } else {
+            o[0] = __uint_as_float(u[k].x), o[1] = __uint_as_float(u[k].y);
+            o[2] = __uint_as_float(u[k].z), o[3] = __uint_as_float(u[k].w);
+            o[4] = __uint_as_float(v[k].x), o[5] = __uint_as_float(v[k].y);
+            o[6] = __uint_as_float(v[k].z), o[7] = __uint_as_float(v[k].w);
+        }
+        float s = dot8(w[k], o);
+#pragma unroll
+        for (int x = LPR / 2; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
+        if (l == k) d = s;
+    }
+    if (l < N) {
+        const int i = first + l * (256 / LPR);
+        const int64_t r = (int64_t)bh * a.blocks * kPrepRows + i;
         float lse = INFINITY;
-        if (live) {
-            const int64_t at = bh * a.Sq + i;
+        if (i < a.Sq) {
+            const int64_t at = (int64_t)bh * a.Sq + i;
             lse = a.lse[at];
             if (a.dlse && lse != -INFINITY) d -= a.dlse[at];
             lse = lse == -INFINITY ? INFINITY : lse;
+        } else {
+            d = 0.f;
         }
         a.nlse2[r] = -lse * kLog2e;
         a.ndelta[r] = -d;
@@ -849,10 +888,10 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const PrepArgs a) {
             // In units of q.k; a row that sees nothing gets bf16's lowest
             // value, which takes any finite score far below the exponential's
             // range (an infinity would leave NaN in the split).
-            uint16_t l[3] = {0xff7fu, 0, 0}, e[3];
-            if (lse != INFINITY) split3(-lse * a.inv_scale, l);
+            uint16_t s[3] = {0xff7fu, 0, 0}, e[3];
+            if (lse != INFINITY) split3(-lse * a.inv_scale, s);
             split3(-d, e);
-            a.ext[r] = make_uint4(l[0] | (uint32_t)l[1] << 16, l[2] | (uint32_t)e[0] << 16, e[1] | (uint32_t)e[2] << 16, 0);
+            a.ext[r] = make_uint4(s[0] | (uint32_t)s[1] << 16, s[2] | (uint32_t)e[0] << 16, e[1] | (uint32_t)e[2] << 16, 0);
         }
     }
 }
@@ -883,8 +922,17 @@ template <int DK, int DV, bool MODS>
 cudaError_t launch_tiles(const BwdLaunch &L, const BwdArgs &a, int num_sms, cudaStream_t stream) {
     using K = BwdKernel<DK, DV, MODS>;
     auto kern = bwd_tile_kernel<DK, DV, MODS>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, K::SMEM_BYTES);
+    // The kernel's shared-memory limit, once a device (a call costs 1 us).
+    static std::atomic<uint64_t> set{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (!(set.load(std::memory_order_relaxed) & bit) || !bit) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, K::SMEM_BYTES);
+        if (e != cudaSuccess) return e;
+        set.fetch_or(bit, std::memory_order_relaxed);
+    }
     const int grid = a.items < num_sms ? a.items : num_sms;
     if (grid == 0) return cudaSuccess;
     kern<<<grid, K::THREADS, K::SMEM_BYTES, stream>>>(L.tmQx, L.tmKx, L.tmVx, L.tmDOx, L.tmQy, L.tmKy, L.tmVy, L.tmDOy, a);
@@ -900,17 +948,19 @@ cudaError_t launch_bwd(const BwdLaunch &L, int num_sms, cudaStream_t stream) {
         p.o = L.o, p.dout = static_cast<const __nv_bfloat16 *>(L.dout), p.lse = L.lse, p.dlse = L.dlse;
         p.o_sb = L.o_sb, p.o_sh = L.o_sh, p.o_ss = L.o_ss;
         p.do_sb = L.do_sb, p.do_sh = L.do_sh, p.do_ss = L.do_ss;
-        p.Hq = L.Hq, p.Sq = L.Sq, p.o_bf16 = L.o_bf16;
-        p.pitch = pitch > 0 ? pitch : 1, p.rows = (int64_t)L.B * L.Hq * pitch;
+        p.Hq = L.Hq, p.Sq = L.Sq;
+        p.blocks = (int)(pitch / kPrepRows);
         p.nlse2 = L.nlse2, p.ndelta = L.ndelta;
         p.ext = L.has_mods ? nullptr : static_cast<uint4 *>(L.ext), p.inv_scale = 1.f / L.scale;
         p.next = L.next;
-        const int per = 256 / (L.dv / 8);
-        const unsigned grid = (unsigned)((p.rows + per - 1) / per);
+        unsigned grid = (unsigned)(L.B * L.Hq) * (unsigned)p.blocks;
+        if (grid == 0) grid = 1, p.blocks = 0;  // the counter alone
         if (L.dv == 64)
-            bwd_prep_kernel<64><<<grid > 0 ? grid : 1, 256, 0, stream>>>(p);
+            L.o_bf16 ? bwd_prep_kernel<64, true><<<grid, 256, 0, stream>>>(p)
+                     : bwd_prep_kernel<64, false><<<grid, 256, 0, stream>>>(p);
         else
-            bwd_prep_kernel<128><<<grid > 0 ? grid : 1, 256, 0, stream>>>(p);
+            L.o_bf16 ? bwd_prep_kernel<128, true><<<grid, 256, 0, stream>>>(p)
+                     : bwd_prep_kernel<128, false><<<grid, 256, 0, stream>>>(p);
         cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }

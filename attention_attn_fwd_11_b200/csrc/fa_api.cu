@@ -1069,7 +1069,10 @@ fa_status fa_bwd(const fa_bwd_params *p, void *stream) {
     const auto both = [&](CUtensorMap *x, CUtensorMap *y, const void *t, int d, int S, int H, int64_t ss, int64_t sh,
                           int64_t sb, const char *name) {
         fa_status r = encode_4d(x, t, d, S, H, p->B, ss, sh, sb, 128, name);
-        return r == FA_OK ? encode_4d(y, t, d, S, H, p->B, ss, sh, sb, fa::bwd_walk(p->dk), name) : r;
+        if (r != FA_OK) return r;
+        *y = *x;
+        return fa::bwd_walk(p->dk) == 128 ? FA_OK
+                                          : encode_4d(y, t, d, S, H, p->B, ss, sh, sb, fa::bwd_walk(p->dk), name);
     };
     if (rows) {
         st = both(&L.tmQx, &L.tmQy, p->q, p->dk, p->Sq, p->Hq, p->q_ss, p->q_sh, p->q_sb, "fa_bwd q");

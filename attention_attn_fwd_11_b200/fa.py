@@ -173,8 +173,8 @@ def _ptr(t):
 
 
 def _stream(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the current stream's handle, without building a Stream object (3 us)
+        return _vp(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
     return _vp(stream.cuda_stream)
 
 
@@ -186,17 +186,18 @@ def _need_cuda(*ts):
 
 def _need_current_device(*ts):
     """CUDA tensors of one device, the current one (the library launches there)."""
-    _need_cuda(*ts)
+    current = torch.cuda.current_device() if torch.cuda.is_available() else -1
     for t in ts:
-        if t is not None and t.device.index != torch.cuda.current_device():
+        if t is not None and (t.get_device() != current or current < 0):
+            _need_cuda(t)
             raise ValueError("every tensor must be on the current CUDA device (see torch.cuda.device)")
 
 
 def _odt(dtype):
-    if dtype == torch.float32:
-        return FA_F32
     if dtype == torch.bfloat16:
         return FA_BF16
+    if dtype == torch.float32:
+        return FA_F32
     raise ValueError("output dtype must be float32 or bfloat16")
 
 
@@ -292,37 +293,45 @@ def bwd(q, k, v, o, lse, do, scale=None, causal=False, mask=None, max_bias=0.0, 
     for t in (q, k, v, do):
         if t.dtype != torch.bfloat16 or t.dim() != 4 or t.stride(3) != 1:
             raise ValueError("q, k, v and do must be 4-D bf16 with a contiguous last dim")
-    B, Hq, Sq, hd = q.shape
-    Hkv, Sk, vd = v.shape[1:]
-    if tuple(k.shape) != (B, Hkv, Sk, hd) or v.shape[0] != B:
+    qs, ks, vs, os = q.shape, k.shape, v.shape, o.shape
+    B, Hq, Sq, hd = qs
+    _, Hkv, Sk, vd = vs
+    if ks != (B, Hkv, Sk, hd) or vs[0] != B:
         raise ValueError("k must be [B, Hkv, Sk, dk] and v [B, Hkv, Sk, dv] with q's B and dk")
-    if tuple(o.shape) != (B, Hq, Sq, vd) or o.shape != do.shape or o.stride(3) != 1:
+    if os != (B, Hq, Sq, vd) or os != do.shape or o.stride(3) != 1:
         raise ValueError("o and do must be [B, Hq, Sq, dv] with a contiguous last dim")
     for t in (lse, dlse):
-        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (B, Hq, Sq) or not t.is_contiguous()):
+        if t is not None and (t.dtype != torch.float32 or t.shape != (B, Hq, Sq) or not t.is_contiguous()):
             raise ValueError("lse and dlse must be contiguous float32 [B, Hq, Sq]")
     if mask is not None and (mask.dtype != torch.float16 or mask.dim() != 4 or mask.stride(3) != 1 or
                              mask.shape[0] not in (1, B) or mask.shape[1] not in (1, Hq) or
-                             tuple(mask.shape[2:]) != (Sq, Sk)):
+                             mask.shape[2:] != (Sq, Sk)):
         raise ValueError("mask must be [1|B, 1|Hq, Sq, Sk] float16 with a contiguous last dim")
     if sinks is not None and (sinks.dtype != torch.float32 or sinks.shape != (Hq,) or not sinks.is_contiguous()):
         raise ValueError("sinks must be a contiguous float32 tensor of shape [Hq]")
-    dq, dk, dv = (torch.empty(t.shape, device=q.device, dtype=grad_dtype) if g is None else g
-                  for t, g in ((q, dq), (k, dk), (v, dv)))
-    for t, g in ((q, dq), (k, dk), (v, dv)):
-        if g.shape != t.shape or g.stride(3) != 1 or g.dtype != dq.dtype:
+    if dq is None:
+        dq = torch.empty_like(q, dtype=grad_dtype)
+    if dk is None:
+        dk = torch.empty_like(k, dtype=grad_dtype)
+    if dv is None:
+        dv = torch.empty_like(v, dtype=grad_dtype)
+    for g, shape in ((dq, qs), (dk, ks), (dv, vs)):
+        if g.shape != shape or g.stride(3) != 1 or g.dtype != dq.dtype:
             raise ValueError("dq, dk and dv must have the shapes of q, k and v, one dtype and a contiguous last dim")
-    p = _bwd_sizes(q, k, v)
-    p.q, p.k, p.v, p.o, p.dout, p.lse, p.dlse = (_ptr(t) for t in (q, k, v, o, do, lse, dlse))
-    p.gq, p.gk, p.gv = _ptr(dq), _ptr(dk), _ptr(dv)
-    p.q_sb, p.q_sh, p.q_ss = q.stride()[:3]
-    p.k_sb, p.k_sh, p.k_ss = k.stride()[:3]
-    p.v_sb, p.v_sh, p.v_ss = v.stride()[:3]
-    p.o_sb, p.o_sh, p.o_ss = o.stride()[:3]
-    p.do_sb, p.do_sh, p.do_ss = do.stride()[:3]
-    p.gq_sb, p.gq_sh, p.gq_ss = dq.stride()[:3]
-    p.gk_sb, p.gk_sh, p.gk_ss = dk.stride()[:3]
-    p.gv_sb, p.gv_sh, p.gv_ss = dv.stride()[:3]
+    p = BwdParams()
+    p.B, p.Hq, p.Hkv, p.Sq, p.Sk, p.dk, p.dv = B, Hq, Hkv, Sq, Sk, hd, vd
+    p.q, p.k, p.v, p.o, p.dout, p.lse = (q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(),
+                                         lse.data_ptr())
+    p.gq, p.gk, p.gv = dq.data_ptr(), dk.data_ptr(), dv.data_ptr()
+    p.dlse = _ptr(dlse)
+    p.q_sb, p.q_sh, p.q_ss, _ = q.stride()
+    p.k_sb, p.k_sh, p.k_ss, _ = k.stride()
+    p.v_sb, p.v_sh, p.v_ss, _ = v.stride()
+    p.o_sb, p.o_sh, p.o_ss, _ = o.stride()
+    p.do_sb, p.do_sh, p.do_ss, _ = do.stride()
+    p.gq_sb, p.gq_sh, p.gq_ss, _ = dq.stride()
+    p.gk_sb, p.gk_sh, p.gk_ss, _ = dk.stride()
+    p.gv_sb, p.gv_sh, p.gv_ss, _ = dv.stride()
     p.scale = 1.0 / math.sqrt(hd) if scale is None else scale
     p.causal = 1 if causal else 0
     p.o_dtype, p.g_dtype = _odt(o.dtype), _odt(dq.dtype)
@@ -336,12 +345,14 @@ def bwd(q, k, v, o, lse, do, scale=None, causal=False, mask=None, max_bias=0.0, 
     if sinks is not None:
         dsinks = torch.empty_like(sinks)
         p.sinks, p.gsinks = _ptr(sinks), _ptr(dsinks)
+    lib = load()
+    ref = ctypes.byref(p)
     if workspace is None:
         n = ctypes.c_size_t(0)
-        _check(load().fa_bwd_workspace_size(ctypes.byref(p), ctypes.byref(n)))
-        workspace = torch.empty(max(n.value, 256), device=q.device, dtype=torch.uint8)
-    p.workspace, p.workspace_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
-    _check(load().fa_bwd(ctypes.byref(p), _stream(stream)))
+        _check(lib.fa_bwd_workspace_size(ref, ctypes.byref(n)))
+        workspace = torch.empty(n.value, device=q.device, dtype=torch.uint8)
+    p.workspace, p.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _check(lib.fa_bwd(ref, _stream(stream)))
     return (dq, dk, dv) if sinks is None else (dq, dk, dv, dsinks)
 
 
@@ -727,14 +738,14 @@ def _check_inv_freq(inv_freq):
 
 def _check_pos(pos, B, S):
     """Pitch of pos over the batch (0 broadcasts)."""
-    if pos.dtype != torch.int32 or (S > 1 and pos.stride(-1) != 1) or tuple(pos.shape) not in ((S,), (1, S), (B, S)):
+    if pos.dtype != torch.int32 or (S > 1 and pos.stride(-1) != 1) or pos.shape not in ((B, S), (S,), (1, S)):
         raise ValueError("pos must be an int32 tensor [S], [1, S] or [B, S] with a contiguous last dim")
     return pos.stride(0) if pos.dim() == 2 and pos.shape[0] > 1 else 0
 
 
 def _rope_out(x, out):
     if out is None:
-        return torch.empty(x.shape, device=x.device, dtype=x.dtype)
+        return torch.empty_like(x, memory_format=torch.contiguous_format)
     if out.shape != x.shape or out.dtype != x.dtype or out.stride(3) != 1:
         raise ValueError("an output must have its input's shape and dtype and a contiguous last dim")
     return out
@@ -751,8 +762,8 @@ def rope(q, inv_freq, k=None, pos=None, pos0=0, interleaved=False, offset=0, inv
     given, also as q / k themselves.  Returns (q turned, k turned or None)."""
     _need_current_device(q, k, pos, out, k_out)
     for t in (q, k):
-        if t is not None and (t.dtype not in (torch.bfloat16, torch.float32) or t.dim() != 4 or t.stride(3) != 1 or
-                              t.dtype != q.dtype):
+        if t is not None and (t.dim() != 4 or t.stride(3) != 1 or t.dtype != q.dtype or
+                              t.dtype not in (torch.bfloat16, torch.float32)):
             raise ValueError("q and k must be 4-D tensors of one dtype, bf16 or fp32, with a contiguous last dim")
     if k is not None and (k.shape[0], k.shape[2], k.shape[3]) != (q.shape[0], q.shape[2], q.shape[3]):
         raise ValueError("k must be [B, Hk, S, d] with q's B, S and d")
@@ -762,15 +773,15 @@ def rope(q, inv_freq, k=None, pos=None, pos0=0, interleaved=False, offset=0, inv
     B, Hq, S, d = q.shape
     out = _rope_out(q, out)
     p = RopeParams()
-    p.q, p.q_out = _ptr(q), _ptr(out)
-    p.q_sb, p.q_sh, p.q_ss = q.stride()[:3]
-    p.qo_sb, p.qo_sh, p.qo_ss = out.stride()[:3]
+    p.q, p.q_out = q.data_ptr(), out.data_ptr()
+    p.q_sb, p.q_sh, p.q_ss, _ = q.stride()
+    p.qo_sb, p.qo_sh, p.qo_ss, _ = out.stride()
     p.B, p.Hq, p.S, p.d = B, Hq, S, d
     if k is not None:
         k_out = _rope_out(k, k_out)
         p.k, p.k_out, p.Hk = _ptr(k), _ptr(k_out), k.shape[1]
-        p.k_sb, p.k_sh, p.k_ss = k.stride()[:3]
-        p.ko_sb, p.ko_sh, p.ko_ss = k_out.stride()[:3]
+        p.k_sb, p.k_sh, p.k_ss, _ = k.stride()
+        p.ko_sb, p.ko_sh, p.ko_ss, _ = k_out.stride()
     p.dtype = _odt(q.dtype)
     if pos is not None:
         p.pos_sb = _check_pos(pos, B, S)
@@ -796,39 +807,41 @@ def kv_append(k, v, k_cache, v_cache, block_table, seq_lens, q_lens=None, inv_fr
     sequence; q [B,Hq,Sq,dk], if given, is turned too.  Returns q turned (in
     q_out, which may be q; rows past q_lens are zeros), or None without q."""
     _need_current_device(k, v, k_cache, v_cache, block_table, seq_lens, q_lens, q, q_out, pos)
-    for t in (k, v) + ((q,) if q is not None else ()):
-        if t.dtype != torch.bfloat16 or t.dim() != 4 or t.stride(3) != 1:
+    for t in (k, v, q):
+        if t is not None and (t.dtype != torch.bfloat16 or t.dim() != 4 or t.stride(3) != 1):
             raise ValueError("k, v and q must be 4-D bf16 with a contiguous last dim")
     if k.shape[:3] != v.shape[:3]:
         raise ValueError("k and v must have one B, Hkv and Sq")
     B, Hkv, Sq, dk = k.shape
     dv = v.shape[3]
-    for c, d in ((k_cache, dk), (v_cache, dv)):
-        if c.dim() != 4 or not c.is_contiguous() or c.shape[1] != Hkv or c.shape[:3] != k_cache.shape[:3]:
-            raise ValueError("the caches must be contiguous [num_blocks, Hkv, block_size, row] with k's Hkv")
-        if c.dtype != k_cache.dtype or c.dtype not in (torch.bfloat16, torch.uint8):
-            raise ValueError("the caches must both be bf16, or both uint8 rows of a quantised type")
-        if c.dtype == torch.bfloat16 and c.shape[3] != d:
-            raise ValueError("the rows of a bf16 cache must be as wide as those of k and v")
+    cs, cvs, ctype = k_cache.shape, v_cache.shape, k_cache.dtype
+    if (len(cs) != 4 or len(cvs) != 4 or cs[1] != Hkv or cs[:3] != cvs[:3] or not k_cache.is_contiguous() or
+            not v_cache.is_contiguous()):
+        raise ValueError("the caches must be contiguous [num_blocks, Hkv, block_size, row] with k's Hkv")
+    if v_cache.dtype != ctype or ctype not in (torch.bfloat16, torch.uint8):
+        raise ValueError("the caches must both be bf16, or both uint8 rows of a quantised type")
+    if ctype == torch.bfloat16 and (cs[3] != dk or cvs[3] != dv):
+        raise ValueError("the rows of a bf16 cache must be as wide as those of k and v")
     p = KvAppendParams()
-    if k_cache.dtype == torch.uint8:
+    if ctype == torch.uint8:
         kv_type, _ = _paged_kv(k, k_cache, kv_type)
-        if any(c.shape[3] != d // 32 * KV_QUANT[kv_type][1] for c, d in ((k_cache, dk), (v_cache, dv))):
+        per = KV_QUANT[kv_type][1]
+        if cs[3] != dk // 32 * per or cvs[3] != dv // 32 * per:
             raise ValueError("the cache rows do not hold k's and v's rows as " + kv_type)
         p.kv_type, p.k_scale, p.v_scale = KV_QUANT[kv_type][0], k_scale, v_scale
     elif kv_type is not None:
         raise ValueError("kv_type is for uint8 caches")
-    for t in (block_table, seq_lens) + ((q_lens,) if q_lens is not None else ()):
-        if t.dtype != torch.int32 or not t.is_contiguous() or t.shape[0] != B or t.dim() != (2 if t is block_table else 1):
+    for t, dim in ((block_table, 2), (seq_lens, 1), (q_lens, 1)):
+        if t is not None and (t.dtype != torch.int32 or t.dim() != dim or t.shape[0] != B or not t.is_contiguous()):
             raise ValueError("block_table [B, max_blocks], seq_lens [B] and q_lens [B] must be contiguous int32")
-    p.k, p.v = _ptr(k), _ptr(v)
-    p.k_sb, p.k_sh, p.k_ss = k.stride()[:3]
-    p.v_sb, p.v_sh, p.v_ss = v.stride()[:3]
-    p.k_cache, p.v_cache = _ptr(k_cache), _ptr(v_cache)
-    p.block_table, p.seq_lens, p.q_lens = _ptr(block_table), _ptr(seq_lens), _ptr(q_lens)
+    p.k, p.v = k.data_ptr(), v.data_ptr()
+    p.k_sb, p.k_sh, p.k_ss, _ = k.stride()
+    p.v_sb, p.v_sh, p.v_ss, _ = v.stride()
+    p.k_cache, p.v_cache = k_cache.data_ptr(), v_cache.data_ptr()
+    p.block_table, p.seq_lens, p.q_lens = block_table.data_ptr(), seq_lens.data_ptr(), _ptr(q_lens)
     p.max_blocks_per_seq = block_table.shape[1]
     p.B, p.Hkv, p.Sq, p.dk, p.dv = B, Hkv, Sq, dk, dv
-    p.block_size, p.num_blocks = k_cache.shape[2], k_cache.shape[0]
+    p.block_size, p.num_blocks = cs[2], cs[0]
     p.mscale = mscale
     if inv_freq is not None:
         _check_inv_freq(inv_freq)
@@ -843,9 +856,9 @@ def kv_append(k, v, k_cache, v_cache, block_table, seq_lens, q_lens=None, inv_fr
         if (q.shape[0], q.shape[2], q.shape[3]) != (B, Sq, dk):
             raise ValueError("q must be [B, Hq, Sq, dk] with k's B, Sq and dk")
         q_out = _rope_out(q, q_out)
-        p.q, p.q_out, p.Hq = _ptr(q), _ptr(q_out), q.shape[1]
-        p.q_sb, p.q_sh, p.q_ss = q.stride()[:3]
-        p.qo_sb, p.qo_sh, p.qo_ss = q_out.stride()[:3]
+        p.q, p.q_out, p.Hq = q.data_ptr(), q_out.data_ptr(), q.shape[1]
+        p.q_sb, p.q_sh, p.q_ss, _ = q.stride()
+        p.qo_sb, p.qo_sh, p.qo_ss, _ = q_out.stride()
     elif q_out is not None:
         raise ValueError("q_out without q")
     _check(load().fa_kv_append(ctypes.byref(p), _stream(stream)))
