@@ -176,11 +176,20 @@ struct Ring {
     }
 };
 
-#ifndef FA_POLY
-#define FA_POLY 4
-#endif
 // Of every eight exponentials, this many go to the FMA pipe (exp2_poly2).
-constexpr int kPolyOf8 = FA_POLY;
+// 0, 2, 4 and 6 measured (B2 H16 S2048 d128: 132, 128, 130 and 140 us): the
+// tensor cores leave less time than either pipe needs alone.
+constexpr int kPolyOf8 = 2;
+
+// Two exponentials, pair k of the eight.
+FA_DEV void exp2_pair(int k, float e0, float e1, float &p0, float &p1) {
+    if (k % 8 < kPolyOf8) {
+        exp2_poly2(e0, e1, p0, p1);
+    } else {
+        p0 = ex2(e0);
+        p1 = ex2(e1);
+    }
+}
 
 // What every role of a CTA shares.
 struct BwdCta {
@@ -450,6 +459,7 @@ struct BwdWorker {
         const int shift = a.Sk - a.Sq;
         const bool capped = MODS && a.mods.softcap != 0.f;
         const bool masked = MODS && a.mods.mask != nullptr;
+        const float inv_cap = capped ? 1.f / (a.mods.softcap * kLog2e) : 0.f;
         float row_nlse = 0.f, row_ndelta = 0.f;
         if (!KV) {  // rows past Sq are padded in the workspace
             const int64_t r = ((int64_t)it.b * a.Hq + it.h) * a.pitch + xr;
@@ -465,6 +475,38 @@ struct BwdWorker {
         for (int t = 0; t < it.n; ++t) {
             const int y0 = (it.y_first + y) * BN + wg * 32;  // first column: query or key
             const float *sl = reinterpret_cast<const float *>(c.smem + C::OFF_ROW + r1.s * C::ROW_BYTES) + wg * 32;
+            // The tile's mask values (f16 pairs), asked for before its scores
+            // are waited for.  Rows and keys past the end read the last one's:
+            // their P is 0, or their results are not stored.
+            [[maybe_unused]] uint32_t mk[16];
+            if constexpr (MODS) {
+                if (masked) {
+                    const uint16_t *m = reinterpret_cast<const uint16_t *>(a.mods.mask) + (int64_t)it.b * a.mods.m_sb +
+                                        (int64_t)hq * a.mods.m_sh;
+                    if (KV) {
+                        m += min(xr, a.Sk - 1);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            mk[i] = (uint32_t)__ldg(m + (int64_t)min(y0 + 2 * i, a.Sq - 1) * a.mods.m_ss) |
+                                    (uint32_t)__ldg(m + (int64_t)min(y0 + 2 * i + 1, a.Sq - 1) * a.mods.m_ss) << 16;
+                    } else {
+                        m += (int64_t)min(xr, a.Sq - 1) * a.mods.m_ss;
+                        if (y0 + 32 <= a.Sk) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const uint4 w = __ldg(reinterpret_cast<const uint4 *>(m + y0) + i);
+                                mk[4 * i] = w.x, mk[4 * i + 1] = w.y, mk[4 * i + 2] = w.z, mk[4 * i + 3] = w.w;
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                mk[i] = (uint32_t)__ldg(m + min(y0 + 2 * i, a.Sk - 1)) |
+                                        (uint32_t)__ldg(m + min(y0 + 2 * i + 1, a.Sk - 1)) << 16;
+                        }
+                    }
+                }
+            }
+            const float slope = MODS ? alibi_slope(a.mods, hq) * kLog2e : 0.f;
             if (KV && MODS && !c.wait(bars + C::FULL1 + r1.s, r1.ph)) return false;
             if (!c.wait(bars + B_SFULL, tiles & 1u)) return false;
             tc_fence_after();
@@ -478,65 +520,20 @@ struct BwdWorker {
                 for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(r[i]);
             }
             if (!C::ALIAS) arrive(c, bars + B_SREAD, lane);
-            float cap[MODS ? 32 : 1];  // ds/dz under a softcap
-            if constexpr (MODS) {
-                const float slope = alibi_slope(a.mods, hq) * kLog2e;
-                if (capped) {
-                    const float inv = 1.f / (a.mods.softcap * kLog2e);
-#pragma unroll
-                    for (int i = 0; i < 32; i += 4) softcap4(x + i, a.scale, a.mods.softcap);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const float th = x[i] * inv;
-                        cap[i] = fmaf(-th, th, 1.f) * a.mods.softcap;
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) x[i] *= a.scale_log2;
-                }
-                if (masked) {
-                    // Rows and keys past the end read the last one's values:
-                    // their P is 0, or their results are not stored.
-                    const __half *m = a.mods.mask + (int64_t)it.b * a.mods.m_sb + (int64_t)hq * a.mods.m_sh;
-                    if (KV) {
-                        m += min(xr, a.Sk - 1);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            x[i] = fmaf(__half2float(m[(int64_t)min(y0 + i, a.Sq - 1) * a.mods.m_ss]), slope, x[i]);
-                    } else {
-                        m += (int64_t)min(xr, a.Sq - 1) * a.mods.m_ss;
-                        if (y0 + 32 <= a.Sk) {
-#pragma unroll
-                            for (int i = 0; i < 32; i += 8) {
-                                const uint4 w = __ldg(reinterpret_cast<const uint4 *>(m + y0 + i));
-                                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) {
-                                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&u[j]));
-                                    x[i + 2 * j] = fmaf(f.x, slope, x[i + 2 * j]);
-                                    x[i + 2 * j + 1] = fmaf(f.y, slope, x[i + 2 * j + 1]);
-                                }
-                            }
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                x[i] = fmaf(__half2float(m[min(y0 + i, a.Sk - 1)]), slope, x[i]);
-                        }
-                    }
-                }
-            }
             const bool edge = KV ? (a.causal && y0 < x0 + 127 - shift)
                                  : (y0 + 32 > min(a.Sk, a.causal ? x0 + shift + 1 : a.Sk));
-            if (edge) {
+            const auto hide = [&](float (&v)[4], int i) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    if (KV ? (y0 + i < lim_lo) : (y0 + i >= lim_hi)) x[i] = -INFINITY;
-            }
-            // P
+                for (int j = 0; j < 4; ++j)
+                    if (KV ? (y0 + i + j < lim_lo) : (y0 + i + j >= lim_hi)) v[j] = -INFINITY;
+            };
+            // P (and under a softcap P ds/dz in its place in x)
             uint32_t pk[16];
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
-                uint64_t nl[2];
+                float v[4] = {x[i], x[i + 1], x[i + 2], x[i + 3]};
+                float cap[4] = {1.f, 1.f, 1.f, 1.f};
+                uint64_t nl[2];  // -LSE of the four, in base 2
                 if (C::EXT) {
                     nl[0] = nl[1] = 0;
                 } else if (KV) {
@@ -545,19 +542,37 @@ struct BwdWorker {
                 } else {
                     nl[0] = nl[1] = f2_pack(row_nlse, row_nlse);
                 }
+                if constexpr (MODS) {
+                    if (capped) {
+                        softcap4(v, a.scale, a.mods.softcap);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float th = v[j] * inv_cap;
+                            cap[j] = fmaf(-th, th, 1.f) * a.mods.softcap;
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) v[j] *= a.scale_log2;
+                    }
+                    if (masked) {
+#pragma unroll
+                        for (int j = 0; j < 4; j += 2) {
+                            const float2 m = __half22float2(*reinterpret_cast<const __half2 *>(&mk[(i + j) / 2]));
+                            v[j] = fmaf(m.x, slope, v[j]);
+                            v[j + 1] = fmaf(m.y, slope, v[j + 1]);
+                        }
+                    }
+                }
+                if (edge) hide(v, i);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const int k = i + 2 * j;
-                    const uint64_t xx = f2_pack(x[k], x[k + 1]);
+                    const uint64_t xx = f2_pack(v[2 * j], v[2 * j + 1]);
                     float e0, e1;
                     f2_unpack(C::EXT ? f2_mul(xx, sc2) : MODS ? f2_add(xx, nl[j]) : f2_fma(xx, sc2, nl[j]), e0, e1);
-                    if (k % 8 < kPolyOf8) {
-                        exp2_poly2(e0, e1, x[k], x[k + 1]);
-                    } else {
-                        x[k] = ex2(e0);
-                        x[k + 1] = ex2(e1);
-                    }
+                    exp2_pair(k, e0, e1, x[k], x[k + 1]);
                     pk[k / 2] = pack_bf16x2(x[k], x[k + 1]);
+                    if (capped) x[k] *= cap[2 * j], x[k + 1] *= cap[2 * j + 1];
                 }
             }
             if (KV) {
@@ -569,10 +584,6 @@ struct BwdWorker {
                 tmem_st16(tP, pk);
                 tmem_wait_st();
                 arrive(c, bars + B_PREADY, lane);
-            }
-            if (MODS && capped) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) x[i] *= cap[i];
             }
             // dS
             if (!c.wait(bars + B_TFULL, tiles & 1u)) return false;
