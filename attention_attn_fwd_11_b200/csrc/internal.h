@@ -169,7 +169,7 @@ struct RopeLaunch {
     const int32_t *pos;  // [B, S] at a pitch of pos_sb (0 broadcasts), or NULL: pos0 + s
     int64_t pos_sb;
     int pos0;
-    int items, heads;  // set by launch_rope
+    int items, heads, groups0;  // set by launch_rope
 };
 cudaError_t launch_rope(RopeLaunch L, bool f32, int num_sms, cudaStream_t stream);
 
@@ -185,6 +185,7 @@ struct AppendLaunch {
     int kv_type;  // 0: bf16; 8: q8_0, 4: q4_0, 2: fp8 e4m3
     float k_scale, v_scale;
     int items, heads, q_groups, kv_groups;  // set by launch_kv_append
+    float k_inv, v_inv;
 };
 cudaError_t launch_kv_append(AppendLaunch L, int num_sms, cudaStream_t stream);
 cudaError_t append_device_error(int clear, int *code);

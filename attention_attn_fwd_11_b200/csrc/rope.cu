@@ -18,10 +18,11 @@
 // sincospif.
 //
 // Both kernels move each row once and are bound by HBM.  A thread owns an
-// item of 16 columns: eight pairs, or two 8-column vectors that pass through.
-// It computes its eight sines and cosines once and walks a group of heads
+// item of two 16-byte vectors: their pairs, or columns that pass through.
+// It computes its sines and cosines once and walks a group of heads
 // with them; neighbouring threads own neighbouring vectors, so a warp's
-// loads and stores are whole 128-byte lines.  A thread reads its item before
+// loads and stores are whole 128-byte lines, and has several heads' loads under
+// way at once.  A thread reads its item before
 // it writes it and nobody else touches it, so a tensor may be turned in place.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -39,11 +40,17 @@ __device__ int g_append_err;
 
 constexpr int kThreads = 256;
 
-// Sine and cosine (times mscale) of the eight pairs of item `i`.
-FA_DEV void item_angles(const RopeMap &r, int i, int pos, float (&c)[8], float (&s)[8]) {
+// An item is two 16-byte vectors of V values: V pairs, or 2 V columns that
+// pass through.
+template <typename T>
+constexpr int kVec = 16 / sizeof(T);
+
+// Sine and cosine (times mscale) of the pairs of item `i`.
+template <int V>
+FA_DEV void item_angles(const RopeMap &r, int i, int pos, float (&c)[V], float (&s)[V]) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const uint64_t t = r.turns[8 * i + j] * (uint64_t)(int64_t)pos;
+    for (int j = 0; j < V; ++j) {
+        const uint64_t t = r.turns[V * i + j] * (uint64_t)(int64_t)pos;
         const float half_turns = (float)(int32_t)(uint32_t)(t >> 32) * 0x1p-31f;  // in [-1, 1]
         sincospif(half_turns, &s[j], &c[j]);
         c[j] *= r.mscale;
@@ -51,56 +58,63 @@ FA_DEV void item_angles(const RopeMap &r, int i, int pos, float (&c)[8], float (
     }
 }
 
-// Columns of the two 8-column vectors of item i of a row of width d: items
-// below rot / 16 hold pairs, the others pass through.
+// First columns of the two vectors of item i of a row: items below rot / 2V
+// hold pairs, the others pass through.
+template <int V>
 FA_DEV void item_columns(const RopeMap &r, int i, int &c0, int &c1) {
-    const int ni = r.rot >> 4;
+    const int ni = r.rot / (2 * V);
     if (i < ni) {
-        c0 = r.offset + (r.interleaved ? 16 * i : 8 * i);
-        c1 = c0 + (r.interleaved ? 8 : r.rot >> 1);
+        c0 = r.offset + (r.interleaved ? 2 * V * i : V * i);
+        c1 = c0 + (r.interleaved ? V : r.rot >> 1);
     } else {
-        const int col = 16 * (i - ni);
+        const int col = 2 * V * (i - ni);
         c0 = col < r.offset ? col : col + r.rot;
-        c1 = c0 + 8;
+        c1 = c0 + V;
     }
 }
 
-FA_DEV void load8(const __nv_bfloat16 *p, float (&x)[8]) {
-    const uint4 w = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+// A vector as it lies in memory.  Every value is used once, so loads and
+// stores are marked to leave the caches first.
+template <typename T>
+struct Raw {
+    uint4 w;
+    FA_DEV void load(const T *p) { w = __ldcs(reinterpret_cast<const uint4 *>(p)); }
+    FA_DEV void get(float (&x)[kVec<T>]) const {
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        x[2 * j] = __uint_as_float(u[j] << 16);
-        x[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (sizeof(T) == 2) {
+                x[2 * j] = __uint_as_float(u[j] << 16);
+                x[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
+            } else {
+                x[j] = __uint_as_float(u[j]);
+            }
+        }
     }
+};
+FA_DEV void store_vec(__nv_bfloat16 *p, const float (&x)[8]) {
+    __stcs(reinterpret_cast<uint4 *>(p), make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                                                    pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])));
 }
-FA_DEV void load8(const float *p, float (&x)[8]) {
-    const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
-FA_DEV void store8(__nv_bfloat16 *p, const float (&x)[8]) {
-    *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                               pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-}
-FA_DEV void store8(float *p, const float (&x)[8]) {
-    *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
-    *reinterpret_cast<float4 *>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+FA_DEV void store_vec(float *p, const float (&x)[4]) {
+    __stcs(reinterpret_cast<float4 *>(p), make_float4(x[0], x[1], x[2], x[3]));
 }
 
 // The item's two vectors turned, in 32 bits.
-FA_DEV void turn(bool interleaved, const float (&c)[8], const float (&s)[8], float (&x)[8], float (&y)[8]) {
+template <int V>
+FA_DEV void turn(bool interleaved, const float (&c)[V], const float (&s)[V], float (&x)[V], float (&y)[V]) {
     if (interleaved) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < V / 2; ++j) {
             const float a = x[2 * j], b = x[2 * j + 1], e = y[2 * j], f = y[2 * j + 1];
             x[2 * j] = a * c[j] - b * s[j];
             x[2 * j + 1] = b * c[j] + a * s[j];
-            y[2 * j] = e * c[j + 4] - f * s[j + 4];
-            y[2 * j + 1] = f * c[j + 4] + e * s[j + 4];
+            y[2 * j] = e * c[j + V / 2] - f * s[j + V / 2];
+            y[2 * j + 1] = f * c[j + V / 2] + e * s[j + V / 2];
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < V; ++j) {
             const float a = x[j], b = y[j];
             x[j] = a * c[j] - b * s[j];
             y[j] = b * c[j] + a * s[j];
@@ -110,35 +124,66 @@ FA_DEV void turn(bool interleaved, const float (&c)[8], const float (&s)[8], flo
 
 // ---------------------------------------------------------------- fa_rope --
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeLaunch L) {
-    const int ni = L.map.rot >> 4;
+// Heads whose loads a thread has under way together: enough bytes for HBM
+// (33.5 M bf16 values: 37 us with one head at a time, 30.8 with four).
+constexpr int kBatch = 4;
+
+// Walks heads h0 .. h1 - 1 of one row of t with this thread's item, N heads at
+// a time.  angles: computes the sines, called once, under the first loads.
+// done(h, x, y) takes each head's two vectors; `read` false gives zeros.
+template <typename T, int N, typename Angles, typename Done>
+FA_DEV void walk_heads(const T *src, int64_t sh, int h0, int h1, int c0, int c1, bool read, bool turned, bool interleaved,
+                       const Angles &angles, const Done &done) {
+    constexpr int V = kVec<T>;
+    float cs[V], sn[V];
+    src += (int64_t)h0 * sh;
+    for (int h = h0; h < h1; h += N, src += N * sh) {
+        Raw<T> u[N], w[N];
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            if (read && h + k < h1) {
+                u[k].load(src + k * sh + c0);
+                w[k].load(src + k * sh + c1);
+            }
+        if (turned && h == h0) angles(cs, sn);
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            if (h + k < h1) {
+                float x[V] = {}, y[V] = {};
+                if (read) {
+                    u[k].get(x);
+                    w[k].get(y);
+                    if (turned) turn(interleaved, cs, sn, x, y);
+                }
+                done(h + k, x, y);
+            }
+    }
+}
+
+// blockIdx.x: rows; blockIdx.y: groups of `heads` heads, first those of x[0].
+template <typename T, int N>
+__global__ void __launch_bounds__(kThreads, 2) rope_kernel(const __grid_constant__ RopeLaunch L) {
+    constexpr int V = kVec<T>;
+    const int ni = L.map.rot / (2 * V);
     const int item = threadIdx.x % L.items, tok = threadIdx.x / L.items;
     const int64_t row = (int64_t)blockIdx.x * (kThreads / L.items) + tok;
     if (tok >= kThreads / L.items || row >= (int64_t)L.B * L.S) return;
-    const int b = (int)(row / L.S), s = (int)(row % L.S);
+    const int b = (int)((uint32_t)row / (uint32_t)L.S), s = (int)((uint32_t)row % (uint32_t)L.S);
+    const bool turned = item < ni, second = (int)blockIdx.y >= L.groups0;
+    const RopeTensor &t = L.x[second];
+    if (t.in_place && !turned) return;  // nothing moves
     int c0, c1;
-    item_columns(L.map, item, c0, c1);
-    float cs[8], sn[8];
-    if (item < ni) {
-        const int pos = L.pos ? __ldg(L.pos + b * L.pos_sb + s) : L.pos0 + s;
-        item_angles(L.map, item, pos, cs, sn);
-    }
-    const int h1 = min(L.x[0].H + L.x[1].H, ((int)blockIdx.y + 1) * L.heads);
-    for (int h = blockIdx.y * L.heads; h < h1; ++h) {
-        const int which = h >= L.x[0].H;
-        const RopeTensor &t = L.x[which];
-        if (t.in_place && item >= ni) continue;  // nothing to move
-        const int hh = h - (which ? L.x[0].H : 0);
-        const T *src = static_cast<const T *>(t.src) + b * t.sb + hh * t.sh + s * t.ss;
-        T *dst = static_cast<T *>(t.dst) + b * t.ob + hh * t.oh + s * t.os;
-        float x[8], y[8];
-        load8(src + c0, x);
-        load8(src + c1, y);
-        if (item < ni) turn(L.map.interleaved, cs, sn, x, y);
-        store8(dst + c0, x);
-        store8(dst + c1, y);
-    }
+    item_columns<V>(L.map, item, c0, c1);
+    const int h0 = ((int)blockIdx.y - (second ? L.groups0 : 0)) * L.heads;
+    const int pos = turned && L.pos ? __ldg(L.pos + b * L.pos_sb + s) : L.pos0 + s;
+    T *dst = static_cast<T *>(t.dst) + b * t.ob + s * t.os;
+    walk_heads<T, N>(
+        static_cast<const T *>(t.src) + b * t.sb + s * t.ss, t.sh, h0, min(t.H, h0 + L.heads), c0, c1, true, turned,
+        L.map.interleaved, [&](float(&c)[V], float(&n)[V]) { item_angles(L.map, item, pos, c, n); },
+        [&](int h, const float(&x)[V], const float(&y)[V]) {
+            store_vec(dst + h * t.oh + c0, x);
+            store_vec(dst + h * t.oh + c1, y);
+        });
 }
 
 // ----------------------------------------------------------- fa_kv_append --
@@ -170,34 +215,59 @@ FA_DEV __half block_scale(float d) {
     return __float2half_rn(isfinite(d) ? fminf(fmaxf(d, -65504.f), 65504.f) : NAN);
 }
 
-// Nearest code (ties to even) of x at scale d, within [lo, hi]; 0 where the
-// scale is zero or not a number.
-FA_DEV int code_of(float x, float d, float lo, float hi) {
-    return d != 0.f && !isnan(d) ? (int)fminf(fmaxf(rintf(x / d), lo), hi) : 0;
-}
+// Codes of one block: x / d to the nearest, ties to even, within [lo, hi]; 0
+// where d is zero or not a number.  The quotient is taken by a product with
+// 1 / d and rounded by adding 1.5 * 2^23, whose low bits are then the code;
+// the remainder x - n d, exact in an FMA, tells the few quotients next to a
+// half that the product put on the wrong side.  (Sixteen divisions and
+// conversions a thread cost more than the copy.)
+struct Coder {
+    float d, inv, half, lo, hi;
+    bool ok;
+    FA_DEV Coder(float d_, float lo_, float hi_) : d(d_), lo(lo_), hi(hi_) {
+        ok = d != 0.f && !isnan(d);
+        inv = ok ? 1.f / d : 0.f;
+        half = 0.5f * fabsf(d);
+    }
+    // The code in the low bits (two's complement).
+    FA_DEV uint32_t operator()(float x) const {
+        constexpr float magic = 12582912.f;
+        float r = fminf(fmaxf(x * inv, lo), hi) + magic;
+        float n = r - magic;
+        const float e = fmaf(-n, d, x);
+        if (fabsf(e) >= half && ok) {
+            const float t = d < 0.f ? -e : e;
+            const bool odd = __float_as_uint(r) & 1u;
+            if (t > half || (t == half && odd)) n += 1.f;
+            if (t < -half || (t == -half && odd)) n -= 1.f;
+            r = fminf(fmaxf(n, lo), hi) + magic;
+        }
+        return ok ? __float_as_uint(r) : 0u;
+    }
+};
 
 // Writes the two vectors x (columns c0 ..) and y (columns c1 ..) of a row to
 // the cache row `dst`.  All lanes of a warp call it (it shuffles); `live`
 // says whether this lane's row is written.
 template <int KV>
-FA_DEV void put(uint8_t *dst, int c0, int c1, bool split, float scale, const float (&x)[8], const float (&y)[8],
+FA_DEV void put(uint8_t *dst, int c0, int c1, bool split, float inv, const float (&x)[8], const float (&y)[8],
                 bool live) {
     if constexpr (KV == 0) {
         if (live) {
-            store8(reinterpret_cast<__nv_bfloat16 *>(dst) + c0, x);
-            store8(reinterpret_cast<__nv_bfloat16 *>(dst) + c1, y);
+            store_vec(reinterpret_cast<__nv_bfloat16 *>(dst) + c0, x);
+            store_vec(reinterpret_cast<__nv_bfloat16 *>(dst) + c1, y);
         }
     } else if constexpr (KV == 2) {
-        // e4m3 of x / scale: the quotient in fp32, then one rounding to the
-        // nearest, limited to the type's largest value
+        // e4m3 of x * (1 / scale): the product in fp32, then one rounding to
+        // the nearest, limited to the type's largest value
         uint32_t w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const float(&v)[8] = j < 2 ? x : y;
             const int k = 4 * (j & 1);
-            w[j] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v[k] / scale, v[k + 1] / scale), __NV_SATFINITE,
+            w[j] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v[k] * inv, v[k + 1] * inv), __NV_SATFINITE,
                                                       __NV_E4M3) |
-                   (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v[k + 2] / scale, v[k + 3] / scale),
+                   (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v[k + 2] * inv, v[k + 3] * inv),
                                                       __NV_SATFINITE, __NV_E4M3)
                        << 16;
         }
@@ -214,16 +284,14 @@ FA_DEV void put(uint8_t *dst, int c0, int c1, bool split, float scale, const flo
         for (int v = 0; v < 2; ++v) {
             const int c = v ? c1 : c0;
             const __half h = block_scale(__uint_as_float(v ? k1 : k0) / 127.f);
-            const float d = __half2float(h);
+            const Coder code(__half2float(h), -127.f, 127.f);
             uint8_t *blk = dst + (c >> 5) * 34;
             const int part = (c >> 3) & 3;
             if (live && part == 0) *reinterpret_cast<__half *>(blk) = h;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int q0 = code_of(v ? y[2 * j] : x[2 * j], d, -127.f, 127.f);
-                const int q1 = code_of(v ? y[2 * j + 1] : x[2 * j + 1], d, -127.f, 127.f);
-                if (live)
-                    reinterpret_cast<uint16_t *>(blk + 2 + 8 * part)[j] = (uint16_t)((q0 & 255) | ((q1 & 255) << 8));
+                const uint32_t q0 = code(v ? y[2 * j] : x[2 * j]), q1 = code(v ? y[2 * j + 1] : x[2 * j + 1]);
+                if (live) reinterpret_cast<uint16_t *>(blk + 2 + 8 * part)[j] = (uint16_t)__byte_perm(q0, q1, 0x0040);
             }
         }
     } else {
@@ -246,10 +314,10 @@ FA_DEV void put(uint8_t *dst, int c0, int c1, bool split, float scale, const flo
             const unsigned long long k = v ? k1 : k0;
             const float m = __uint_as_float((uint32_t)(k >> 32) | (uint32_t)(k & 1) << 31);
             h[v] = block_scale(m / -8.f);
-            const float d = __half2float(h[v]);
+            const Coder code(__half2float(h[v]), -8.f, 7.f);
             n[v] = 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) n[v] |= (uint32_t)(code_of(v ? y[j] : x[j], d, -8.f, 7.f) + 8) << (4 * j);
+            for (int j = 0; j < 8; ++j) n[v] |= ((code(v ? y[j] : x[j]) + 8u) & 15u) << (4 * j);
         }
         // Byte j of a block holds values j (low) and j + 16 (high): vectors 0
         // and 2, or 1 and 3, of the block.  Split: lanes 0, 1 of four own the
@@ -292,14 +360,14 @@ FA_DEV void put(uint8_t *dst, int c0, int c1, bool split, float scale, const flo
 
 // blockIdx.x: rows (sequence, new row); blockIdx.y: groups of `heads` heads,
 // first those of q, then of k, then of v.
-template <int KV>
-__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendLaunch L) {
+template <int KV, int N>
+__global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_constant__ AppendLaunch L) {
     const int ni = L.map.rot >> 4;
     const int rows_per_block = kThreads / L.items;
     const int item = threadIdx.x % L.items, tok = threadIdx.x / L.items;
     const int64_t row = (int64_t)blockIdx.x * rows_per_block + tok;
     bool live = tok < rows_per_block && row < (int64_t)L.B * L.Sq;
-    const int b = live ? (int)(row / L.Sq) : 0, i = live ? (int)(row % L.Sq) : 0;
+    const int b = live ? (int)((uint32_t)row / (uint32_t)L.Sq) : 0, i = live ? (int)((uint32_t)row % (uint32_t)L.Sq) : 0;
     int g = blockIdx.y, kind = 0;  // 0: q, 1: k, 2: v
     if (g >= L.q_groups) {
         g -= L.q_groups;
@@ -313,32 +381,23 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     live = live && item < (d >> 4);
     int c0, c1;
     if (kind < 2)
-        item_columns(L.map, item, c0, c1);
+        item_columns<8>(L.map, item, c0, c1);
     else
         c0 = 16 * item, c1 = c0 + 8;
     if (!live) c0 = 0, c1 = 8;
-    float cs[8], sn[8];
-    if (turned && live && i < n) {
-        const int pos = L.pos ? __ldg(L.pos + b * L.pos_sb + i) : (int)at;
-        item_angles(L.map, item, pos, cs, sn);
-    }
+    const int pos = turned && live && i < n && L.pos ? __ldg(L.pos + b * L.pos_sb + i) : (int)at;
+    const auto angles = [&](float(&c)[8], float(&s)[8]) { item_angles(L.map, item, pos, c, s); };
     if (kind == 0) {
         // q: turned rows; the rows past the sequence's new ones are zeros
         if (!live || (i < n && L.q.in_place && !turned)) return;
-        const int h1 = min(L.q.H, (g + 1) * L.heads);
-        for (int h = g * L.heads; h < h1; ++h) {
-            const __nv_bfloat16 *src =
-                static_cast<const __nv_bfloat16 *>(L.q.src) + b * L.q.sb + h * L.q.sh + i * L.q.ss;
-            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(L.q.dst) + b * L.q.ob + h * L.q.oh + i * L.q.os;
-            float x[8] = {}, y[8] = {};
-            if (i < n) {
-                load8(src + c0, x);
-                load8(src + c1, y);
-                if (turned) turn(L.map.interleaved, cs, sn, x, y);
-            }
-            store8(dst + c0, x);
-            store8(dst + c1, y);
-        }
+        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(L.q.dst) + b * L.q.ob + i * L.q.os;
+        walk_heads<__nv_bfloat16, N>(
+            static_cast<const __nv_bfloat16 *>(L.q.src) + b * L.q.sb + i * L.q.ss, L.q.sh, g * L.heads,
+            min(L.q.H, (g + 1) * L.heads), c0, c1, i < n, turned && i < n, L.map.interleaved, angles,
+            [&](int h, const float(&x)[8], const float(&y)[8]) {
+                store_vec(dst + h * L.q.oh + c0, x);
+                store_vec(dst + h * L.q.oh + c1, y);
+            });
         return;
     }
     // A row before its sequence's start has no slot; one past the table's
@@ -357,40 +416,50 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     const RopeTensor &t = kind == 1 ? L.k : L.v;
     const int64_t row_bytes = KV == 8 ? d / 32 * 34 : KV == 4 ? d / 32 * 18 : KV == 2 ? d : 2 * d;
     const bool split = turned && !L.map.interleaved;
-    const int h1 = min(L.Hkv, (g + 1) * L.heads);
-    for (int h = g * L.heads; h < h1; ++h) {
-        float x[8] = {}, y[8] = {};
-        if (live) {
-            const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(t.src) + b * t.sb + h * t.sh + i * t.ss;
-            load8(src + c0, x);
-            load8(src + c1, y);
-            if (turned) turn(L.map.interleaved, cs, sn, x, y);
-        }
-        uint8_t *dst = static_cast<uint8_t *>(t.dst) + (slot0 + (int64_t)h * 64) * row_bytes;
-        put<KV>(dst, c0, c1, split, kind == 1 ? L.k_scale : L.v_scale, x, y, live);
-    }
+    uint8_t *dst = static_cast<uint8_t *>(t.dst) + slot0 * row_bytes;
+    walk_heads<__nv_bfloat16, N>(
+        static_cast<const __nv_bfloat16 *>(t.src) + b * t.sb + i * t.ss, t.sh, g * L.heads,
+        min(L.Hkv, (g + 1) * L.heads), c0, c1, live, turned && live, L.map.interleaved, angles,
+        [&](int h, const float(&x)[8], const float(&y)[8]) {
+            put<KV>(dst + h * 64 * row_bytes, c0, c1, split, kind == 1 ? L.k_inv : L.v_inv, x, y, live);
+        });
 }
 
-// Heads that one thread walks with its sines: up to 8, fewer while that
-// leaves the device's threads idle.
+// Heads that one thread walks with its sines: 8 or 4 (whole batches of loads)
+// while that leaves every SM 512 threads, else one: the work is then too small
+// to fill the device and the shortest thread is the fastest (64 single tokens
+// appended in 4.8 us with one, 5.5 with four).
 int head_group(int64_t units, int heads, int num_sms) {
-    int g = 8;
-    while (g > 1 && units * ((heads + g - 1) / g) < (int64_t)num_sms * 2048) g >>= 1;
-    return g;
+    for (int g = 8; g > 2; g >>= 1)
+        if (units * ((heads + g - 1) / g) >= (int64_t)num_sms * 512) return g;
+    return 1;
+}
+
+template <int N>
+void start_append(const AppendLaunch &L, dim3 grid, cudaStream_t stream) {
+    switch (L.kv_type) {
+        case 0: append_kernel<0, N><<<grid, kThreads, 0, stream>>>(L); break;
+        case 2: append_kernel<2, N><<<grid, kThreads, 0, stream>>>(L); break;
+        case 8: append_kernel<8, N><<<grid, kThreads, 0, stream>>>(L); break;
+        default: append_kernel<4, N><<<grid, kThreads, 0, stream>>>(L); break;
+    }
 }
 
 }  // namespace
 
 cudaError_t launch_rope(RopeLaunch L, bool f32, int num_sms, cudaStream_t stream) {
-    L.items = L.d / 16;
+    L.items = L.d / (f32 ? 2 * kVec<float> : 2 * kVec<__nv_bfloat16>);
     const int H = L.x[0].H + L.x[1].H, per = kThreads / L.items;
     const int64_t rows = (int64_t)L.B * L.S;
     L.heads = head_group(rows * L.items, H, num_sms);
-    const dim3 grid((unsigned)((rows + per - 1) / per), (unsigned)((H + L.heads - 1) / L.heads));
+    L.groups0 = (L.x[0].H + L.heads - 1) / L.heads;
+    const dim3 grid((unsigned)((rows + per - 1) / per), (unsigned)(L.groups0 + (L.x[1].H + L.heads - 1) / L.heads));
     if (f32)
-        rope_kernel<float><<<grid, kThreads, 0, stream>>>(L);
+        L.heads == 1 ? rope_kernel<float, 1><<<grid, kThreads, 0, stream>>>(L)
+                     : rope_kernel<float, kBatch><<<grid, kThreads, 0, stream>>>(L);
     else
-        rope_kernel<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(L);
+        L.heads == 1 ? rope_kernel<__nv_bfloat16, 1><<<grid, kThreads, 0, stream>>>(L)
+                     : rope_kernel<__nv_bfloat16, kBatch><<<grid, kThreads, 0, stream>>>(L);
     return cudaGetLastError();
 }
 
@@ -401,13 +470,13 @@ cudaError_t launch_kv_append(AppendLaunch L, int num_sms, cudaStream_t stream) {
     L.heads = head_group(rows * L.items, L.q.H + 2 * L.Hkv, num_sms);
     L.q_groups = (L.q.H + L.heads - 1) / L.heads;
     L.kv_groups = (L.Hkv + L.heads - 1) / L.heads;
+    L.k_inv = 1.f / L.k_scale;
+    L.v_inv = 1.f / L.v_scale;
     const dim3 grid((unsigned)((rows + per - 1) / per), (unsigned)(L.q_groups + 2 * L.kv_groups));
-    switch (L.kv_type) {
-        case 0: append_kernel<0><<<grid, kThreads, 0, stream>>>(L); break;
-        case 2: append_kernel<2><<<grid, kThreads, 0, stream>>>(L); break;
-        case 8: append_kernel<8><<<grid, kThreads, 0, stream>>>(L); break;
-        default: append_kernel<4><<<grid, kThreads, 0, stream>>>(L); break;
-    }
+    if (L.heads == 1)
+        start_append<1>(L, grid, stream);
+    else
+        start_append<kBatch>(L, grid, stream);
     return cudaGetLastError();
 }
 

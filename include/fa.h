@@ -552,8 +552,8 @@ fa_status fa_rope(const fa_rope_params *p, void *stream);
  *       FA_KV_Q4_0: d = the value of largest magnitude (the first of equals)
  *         / -8, stored as f16; nibble = 8 + (x / d to the nearest, ties to
  *         even, in [-8, 7]);
- *       FA_KV_FP8_E4M3: x / k_scale (or v_scale), limited to +-448, to the
- *         nearest e4m3, ties to even.
+ *       FA_KV_FP8_E4M3: x * (1 / k_scale), or v_scale, in fp32, limited to
+ *         +-448, to the nearest e4m3, ties to even.
  *     d is the f16 that is stored; where it is 0 the codes are 0.  |d| is
  *     limited to 65504; a block with an infinite or NaN value gets d = NaN.
  *   inv_freq, rot_dim, rot_offset, interleaved, mscale: as in fa_rope;
