@@ -72,6 +72,10 @@ struct BwdArgs {
     int g_bf16;
 };
 
+// (dS is ready on two barriers in turn: dQ's workers may finish a tile before
+// the issuer has looked at the one before.)
+enum { B_X1FULL, B_X2FULL, B_X1FREE, B_X2FREE, B_SFULL, B_TFULL, B_SREAD, B_TREAD, B_PREADY, B_DSREADY, B_SETEND = B_DSREADY + 2 };
+
 // Shared and tensor memory of one walk.  TMEM holds the accumulators and one
 // S and one T tile.  Where there is room P and dS get columns of their own, so
 // that S and T are free as soon as they are read.
@@ -113,11 +117,10 @@ struct BwdCfg {
     static_assert(T_END <= TMEM_COLS && T_D + (ALIAS ? BN : BN / 2 + D_COLS) <= TMEM_COLS, "TMEM budget");
     static_assert(T_D >= T_END || ALIAS || T_D + BN <= T_S, "dS apart from S");
     // Barriers of this walk (each kind of item has its own set).
-    static constexpr int FULL1 = 10, EMPTY1 = FULL1 + NST1, FULL2 = EMPTY1 + NST1, EMPTY2 = FULL2 + NST2;
+    static constexpr int FULL1 = B_SETEND, EMPTY1 = FULL1 + NST1, FULL2 = EMPTY1 + NST1, EMPTY2 = FULL2 + NST2;
     static constexpr int BARS = EMPTY2 + NST2;
 };
 
-enum { B_X1FULL, B_X2FULL, B_X1FREE, B_X2FREE, B_SFULL, B_TFULL, B_SREAD, B_TREAD, B_PREADY, B_DSREADY };
 
 template <int DK, int DV, bool MODS>
 struct BwdKernel {
@@ -126,8 +129,9 @@ struct BwdKernel {
     static constexpr int THREADS = 128 + 32 * CK::WARPS;
     static constexpr int OFF_BAR = CK::END > CQ::END ? CK::END : CQ::END;
     // Barriers: the item ring (full, empty), the end of a walk's products, of
-    // all of them, the workers' change from dK / dV to dQ, then both kinds' sets.
-    static constexpr int BAR_DONE = 4, BAR_END = 5, BAR_MOVED = 6, BAR_KV = 7, BAR_Q = BAR_KV + CK::BARS, BARS = BAR_Q + CQ::BARS;
+    // all of them, of the last dK / dV's, the workers' change from dK / dV to
+    // dQ, then both kinds' sets.
+    static constexpr int BAR_DONE = 4, BAR_END = 5, BAR_KVEND = 6, BAR_MOVED = 7, BAR_KV = 8, BAR_Q = BAR_KV + CK::BARS, BARS = BAR_Q + CQ::BARS;
     static constexpr int SMEM_BYTES = OFF_BAR + 8 * BARS + 32 + 1024;  // item ring, TMEM address, flag; alignment slack
     static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 };
@@ -364,7 +368,7 @@ struct BwdIssuer {
             // products that read those.
             if (C::ALIAS && more && !issue_s(c, bars, false, last)) return false;
             if (!KV && more && !issue_t(c, bars, false, last)) return false;
-            if (!c.wait(bars + B_DSREADY, tiles & 1u)) return false;
+            if (!c.wait(bars + B_DSREADY + (int)(tiles & 1u), (tiles >> 1) & 1u)) return false;
             tc_fence_after();
             accumulate<DK>(c.tmem + C::T_A1, c.tmem + C::T_D + (tiles & 1u) * C::D_COLS, c.sbase + C::OFF_Y1 + a1.s * C::Y1_BYTES, t == 0);
             mma_commit_warp(c.bar(bars + C::EMPTY1 + a1.s));
@@ -621,7 +625,7 @@ struct BwdWorker {
             }
             tmem_st16(tD + (tiles & 1u) * C::D_COLS, pk);
             tmem_wait_st();
-            arrive(c, bars + B_DSREADY, lane);
+            arrive(c, bars + B_DSREADY + (int)(tiles & 1u), lane);
             r1.next();
             ++tiles;
             if (++y == it.n_y) y = 0, ++hq;
@@ -681,7 +685,7 @@ bwd_tile_kernel(const __grid_constant__ CUtensorMap tmQx, const __grid_constant_
             if (i == 2 || i == 3) count = 1 + WARPS;  // an item is free once the issuer and the workers have it
             if (i == K::BAR_MOVED) count = WARPS;
             const int j = i >= K::BAR_Q ? i - K::BAR_Q : i - K::BAR_KV;
-            if (i >= K::BAR_KV && j >= B_SREAD && j <= B_DSREADY) count = WARPS;
+            if (i >= K::BAR_KV && j >= B_SREAD && j < B_SETEND) count = WARPS;
             mbar_init(c.bar(i), count);
         }
         *c.abort_flag = 0;
@@ -727,8 +731,7 @@ bwd_tile_kernel(const __grid_constant__ CUtensorMap tmQx, const __grid_constant_
             BwdProducer<CK> pk;
             BwdProducer<CQ> pq;
             int ahead = atomicAdd(a.next, 1);
-            uint32_t kv_walks = 0;
-            bool moved = false;
+            bool kv = false;
             for (int k = 0;; ++k) {
                 const int i = ahead;
                 if (!c.wait1(2 + (k & 1), ((uint32_t)(k >> 1) & 1u) ^ 1u)) break;
@@ -738,13 +741,15 @@ bwd_tile_kernel(const __grid_constant__ CUtensorMap tmQx, const __grid_constant_
                 ahead = atomicAdd(a.next, 1);  // its latency passes under this item
                 if (i < a.kv_items) {
                     const BwdItem it = bwd_item<true, BN>(a, i);
-                    kv_walks += it.n > 0;
+                    kv = true;
                     if (!pk.template item<DK, DV, true>(c, a, it, K::BAR_KV, &tmKx, &tmVx, &tmQy, &tmDOy)) break;
                 } else {
-                    // dQ lays shared memory out anew: the last dK / dV item's
-                    // products must be done with it.
-                    if (!moved && kv_walks > 0 && !c.wait1(K::BAR_DONE, (kv_walks - 1) & 1u)) break;
-                    moved = true;
+                    // dQ lays shared memory out anew: every product of dK and
+                    // dV must be done with it.  (The end of the last walk
+                    // would not do: this lane may be two walks ahead, which
+                    // the parity of a wait cannot tell.)
+                    if (kv && !c.wait1(K::BAR_KVEND, 0)) break;
+                    kv = false;
                     const BwdItem it = bwd_item<false, BN>(a, i);
                     if (!pq.template item<DK, DV, false>(c, a, it, K::BAR_Q, &tmQx, &tmDOx, &tmKy, &tmVy)) break;
                 }
@@ -757,10 +762,14 @@ bwd_tile_kernel(const __grid_constant__ CUtensorMap tmQx, const __grid_constant_
     } else if (warp == 1) {
         BwdIssuer<DK, DV, true, CK> ik;
         BwdIssuer<DK, DV, false, CQ> iq;
+        bool kv = false;
         for (int k = 0, i; (i = take(k)) >= 0; ++k) {
             if (i < a.kv_items) {
+                kv = true;
                 if (!ik.item(c, bwd_item<true, BN>(a, i).n, K::BAR_KV, K::BAR_DONE)) break;
             } else {
+                if (kv) mma_commit_warp(c.bar(K::BAR_KVEND));
+                kv = false;
                 if (!iq.item(c, bwd_item<false, BN>(a, i).n, K::BAR_Q, K::BAR_DONE)) break;
             }
         }

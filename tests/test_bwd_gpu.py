@@ -178,6 +178,27 @@ def test_modifiers(dk, dv, causal):
     run(B, Hq, 3, Sq, Sk, dk, dv, causal, seed=6, mask=per_head, **kw)
 
 
+@pytest.mark.parametrize("dk,dv", PAIRS)
+@pytest.mark.parametrize("S", [128, 256, 300])
+@pytest.mark.parametrize("causal", [False, True])
+def test_many_short_walks(dk, dv, S, causal):
+    """More tiles than SMs, each with one to three tiles to walk: an SM goes through several of dK / dV and on to dQ
+    with hardly any work in between."""
+    for seed in range(3):
+        run(8, 32, 32, S, S, dk, dv, causal, seed=seed, o_dtype=torch.bfloat16)
+
+
+@pytest.mark.parametrize("dk,dv", PAIRS)
+def test_many_walks_again_and_again(dk, dv):
+    q, k, v, do = inputs(2, 16, 16, 2048, 2048, dk, dv, 77)
+    o, lse = fa.fwd(q, k, v, causal=True)
+    first = fa.bwd(q, k, v, o, lse, do, causal=True)
+    check(first, reference(q, k, v, o, lse, do, scale=1 / math.sqrt(dk), causal=True, mask=None, max_bias=0.0, softcap=0.0))
+    for _ in range(20):
+        for a, b in zip(first, fa.bwd(q, k, v, o, lse, do, causal=True)):
+            assert torch.equal(a, b)
+
+
 def test_rows_that_see_nothing_give_zeros():
     q, k, v, do = inputs(1, 2, 2, 300, 130, 128, 128, 3)
     o, lse = fa.fwd(q, k, v, causal=True)
