@@ -180,21 +180,6 @@ struct Ring {
     }
 };
 
-// Of every eight exponentials, this many go to the FMA pipe (exp2_poly2).
-// 0, 2, 4 and 6 measured (B2 H16 S2048 d128: 132, 128, 130 and 140 us): the
-// tensor cores leave less time than either pipe needs alone.
-constexpr int kPolyOf8 = 2;
-
-// Two exponentials, pair k of the eight.
-FA_DEV void exp2_pair(int k, float e0, float e1, float &p0, float &p1) {
-    if (k % 8 < kPolyOf8) {
-        exp2_poly2(e0, e1, p0, p1);
-    } else {
-        p0 = ex2(e0);
-        p1 = ex2(e1);
-    }
-}
-
 // What every role of a CTA shares.
 struct BwdCta {
     uint8_t *smem;
@@ -574,7 +559,8 @@ struct BwdWorker {
                     const uint64_t xx = f2_pack(v[2 * j], v[2 * j + 1]);
                     float e0, e1;
                     f2_unpack(C::EXT ? f2_mul(xx, sc2) : MODS ? f2_add(xx, nl[j]) : f2_fma(xx, sc2, nl[j]), e0, e1);
-                    exp2_pair(k, e0, e1, x[k], x[k + 1]);
+                    x[k] = ex2(e0);
+                    x[k + 1] = ex2(e1);
                     pk[k / 2] = pack_bf16x2(x[k], x[k + 1]);
                     if (capped) x[k] *= cap[2 * j], x[k + 1] *= cap[2 * j + 1];
                 }

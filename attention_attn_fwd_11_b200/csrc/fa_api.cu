@@ -336,10 +336,11 @@ fa_status make_rope_map(const char *who, const double *inv_freq, int rot, int of
     if (!isfinite(mscale)) return fail(FA_ERR_INVALID_ARG, "%s: mscale must be finite", who);
     for (int i = 0; i < rot / 2; ++i) {
         if (!isfinite(inv_freq[i])) return fail(FA_ERR_INVALID_ARG, "%s: inv_freq[%d] is not finite", who, i);
-        // The fraction is below 1 and has at most 64 significant bits, so the scaled value fits.
-        long double x = (long double)inv_freq[i] / 6.283185307179586476925286766559L;
-        x -= floorl(x);
-        m->turns[i] = x < 1.0L ? (uint64_t)ldexpl(x, 64) : 0;
+        // The fraction is below 1 and has at most 64 significant bits, so the
+        // scaled value fits.
+        long double x = (long double)inv_freq[i] * 0.159154943091895335768883763372514362L;  // 1 / (2 pi)
+        if (!(x >= 0.0L && x < 1.0L)) x -= floorl(x);
+        m->turns[i] = x < 1.0L ? (uint64_t)(x * 18446744073709551616.0L) : 0;
     }
     m->rot = rot;
     m->offset = offset;

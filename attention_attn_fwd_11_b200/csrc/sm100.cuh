@@ -609,28 +609,6 @@ FA_DEV uint64_t f2_mul(uint64_t a, uint64_t b) {
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
-// 2^a and 2^b on the FMA pipe, for where the exponential unit is the bound:
-// x = n + f with n the nearest integer (added and taken off again at 1.5 *
-// 2^23, whose low bits then hold n) and |f| <= 1/2, 2^f by a polynomial of
-// degree 4 fitted to the least relative error with p(0) = 1 (2.9e-6), and n
-// added to the exponent bits.  x below -127 counts as -127: f is then 0 and
-// the bits add up to exactly +0, so 2^-inf = 0.  x must be below 127.
-FA_DEV void exp2_poly2(float a, float b, float &ra, float &rb) {
-    const uint64_t magic = f2_pack(12582912.f, 12582912.f), minus = f2_pack(-12582912.f, -12582912.f);
-    const uint64_t x = f2_pack(fmaxf(a, -127.f), fmaxf(b, -127.f));
-    const uint64_t r = f2_add(x, magic);
-    const uint64_t f = f2_fma(f2_add(r, minus), f2_pack(-1.f, -1.f), x);
-    uint64_t p = f2_fma(f, f2_pack(0.009582852944731712f, 0.009582852944731712f),
-                        f2_pack(0.055906426161527634f, 0.055906426161527634f));
-    p = f2_fma(p, f, f2_pack(0.24024099111557007f, 0.24024099111557007f));
-    p = f2_fma(p, f, f2_pack(0.6931241750717163f, 0.6931241750717163f));
-    p = f2_fma(p, f, f2_pack(1.f, 1.f));
-    float p0, p1, n0, n1;
-    f2_unpack(p, p0, p1);
-    f2_unpack(r, n0, n1);
-    ra = __uint_as_float(__float_as_uint(p0) + (__float_as_uint(n0) << 23));
-    rb = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(n1) << 23));
-}
 // Three-input maximum (one instruction).
 FA_DEV float fmax3(float a, float b, float c) {
     float d;

@@ -186,11 +186,13 @@ def _need_cuda(*ts):
 
 def _need_current_device(*ts):
     """CUDA tensors of one device, the current one (the library launches there)."""
-    current = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    current = None
     for t in ts:
-        if t is not None and (t.get_device() != current or current < 0):
+        if t is not None and t.get_device() != current:
             _need_cuda(t)
-            raise ValueError("every tensor must be on the current CUDA device (see torch.cuda.device)")
+            if current is not None or t.get_device() != torch.cuda.current_device():
+                raise ValueError("every tensor must be on the current CUDA device (see torch.cuda.device)")
+            current = t.get_device()
 
 
 def _odt(dtype):
@@ -290,61 +292,58 @@ def bwd(q, k, v, o, lse, do, scale=None, causal=False, mask=None, max_bias=0.0, 
     (dk, dv) head sizes: (64, 64), (128, 128), (192, 128).
     Returns (dq, dk, dv), and with sinks (dq, dk, dv, dsinks [Hq] float32)."""
     _need_current_device(q, k, v, o, lse, do, mask, sinks, dlse, dq, dk, dv, workspace)
-    for t in (q, k, v, do):
-        if t.dtype != torch.bfloat16 or t.dim() != 4 or t.stride(3) != 1:
-            raise ValueError("q, k, v and do must be 4-D bf16 with a contiguous last dim")
+    bf16 = torch.bfloat16
+    if q.dtype != bf16 or k.dtype != bf16 or v.dtype != bf16 or do.dtype != bf16:
+        raise ValueError("q, k, v and do must be bf16")
     qs, ks, vs, os = q.shape, k.shape, v.shape, o.shape
+    if not len(qs) == len(ks) == len(vs) == len(os) == 4:
+        raise ValueError("q, k, v, o and do must be 4-D")
     B, Hq, Sq, hd = qs
     _, Hkv, Sk, vd = vs
     if ks != (B, Hkv, Sk, hd) or vs[0] != B:
         raise ValueError("k must be [B, Hkv, Sk, dk] and v [B, Hkv, Sk, dv] with q's B and dk")
-    if os != (B, Hq, Sq, vd) or os != do.shape or o.stride(3) != 1:
-        raise ValueError("o and do must be [B, Hq, Sq, dv] with a contiguous last dim")
+    if os != (B, Hq, Sq, vd) or os != do.shape:
+        raise ValueError("o and do must be [B, Hq, Sq, dv]")
     for t in (lse, dlse):
         if t is not None and (t.dtype != torch.float32 or t.shape != (B, Hq, Sq) or not t.is_contiguous()):
             raise ValueError("lse and dlse must be contiguous float32 [B, Hq, Sq]")
-    if mask is not None and (mask.dtype != torch.float16 or mask.dim() != 4 or mask.stride(3) != 1 or
-                             mask.shape[0] not in (1, B) or mask.shape[1] not in (1, Hq) or
-                             mask.shape[2:] != (Sq, Sk)):
-        raise ValueError("mask must be [1|B, 1|Hq, Sq, Sk] float16 with a contiguous last dim")
-    if sinks is not None and (sinks.dtype != torch.float32 or sinks.shape != (Hq,) or not sinks.is_contiguous()):
-        raise ValueError("sinks must be a contiguous float32 tensor of shape [Hq]")
     if dq is None:
-        dq = torch.empty_like(q, dtype=grad_dtype)
+        dq = torch.empty_like(q) if grad_dtype == bf16 else torch.empty_like(q, dtype=grad_dtype)
     if dk is None:
-        dk = torch.empty_like(k, dtype=grad_dtype)
+        dk = torch.empty_like(k) if grad_dtype == bf16 else torch.empty_like(k, dtype=grad_dtype)
     if dv is None:
-        dv = torch.empty_like(v, dtype=grad_dtype)
-    for g, shape in ((dq, qs), (dk, ks), (dv, vs)):
-        if g.shape != shape or g.stride(3) != 1 or g.dtype != dq.dtype:
-            raise ValueError("dq, dk and dv must have the shapes of q, k and v, one dtype and a contiguous last dim")
-    p = BwdParams()
-    p.B, p.Hq, p.Hkv, p.Sq, p.Sk, p.dk, p.dv = B, Hq, Hkv, Sq, Sk, hd, vd
-    p.q, p.k, p.v, p.o, p.dout, p.lse = (q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(),
-                                         lse.data_ptr())
-    p.gq, p.gk, p.gv = dq.data_ptr(), dk.data_ptr(), dv.data_ptr()
-    p.dlse = _ptr(dlse)
-    p.q_sb, p.q_sh, p.q_ss, _ = q.stride()
-    p.k_sb, p.k_sh, p.k_ss, _ = k.stride()
-    p.v_sb, p.v_sh, p.v_ss, _ = v.stride()
-    p.o_sb, p.o_sh, p.o_ss, _ = o.stride()
-    p.do_sb, p.do_sh, p.do_ss, _ = do.stride()
-    p.gq_sb, p.gq_sh, p.gq_ss, _ = dq.stride()
-    p.gk_sb, p.gk_sh, p.gk_ss, _ = dk.stride()
-    p.gv_sb, p.gv_sh, p.gv_ss, _ = dv.stride()
-    p.scale = 1.0 / math.sqrt(hd) if scale is None else scale
-    p.causal = 1 if causal else 0
-    p.o_dtype, p.g_dtype = _odt(o.dtype), _odt(dq.dtype)
-    if mask is not None:
-        p.mask = _ptr(mask)
+        dv = torch.empty_like(v) if grad_dtype == bf16 else torch.empty_like(v, dtype=grad_dtype)
+    if dq.shape != qs or dk.shape != ks or dv.shape != vs or dk.dtype != dq.dtype or dv.dtype != dq.dtype:
+        raise ValueError("dq, dk and dv must have the shapes of q, k and v and one dtype")
+    q0, q1, q2, q3 = q.stride()
+    k0, k1, k2, k3 = k.stride()
+    v0, v1, v2, v3 = v.stride()
+    o0, o1, o2, o3 = o.stride()
+    g0, g1, g2, g3 = do.stride()
+    a0, a1, a2, a3 = dq.stride()
+    b0, b1, b2, b3 = dk.stride()
+    c0, c1, c2, c3 = dv.stride()
+    if not q3 == k3 == v3 == o3 == g3 == a3 == b3 == c3 == 1:
+        raise ValueError("the last dim of q, k, v, o, do and the gradients must be contiguous")
+    p = BwdParams(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(), lse.data_ptr(), _ptr(dlse),
+                  dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, Hq, Hkv, Sq, Sk, hd, vd, q0, q1, q2, k0, k1, k2,
+                  v0, v1, v2, o0, o1, o2, g0, g1, g2, a0, a1, a2, b0, b1, b2, c0, c1, c2,
+                  1.0 / math.sqrt(hd) if scale is None else scale, 1 if causal else 0, _odt(o.dtype), _odt(dq.dtype))
+    if mask is not None:  # [Bm, Hm, Sq, Sk] f16; a size-1 batch or head dim broadcasts
+        if (mask.dtype != torch.float16 or mask.dim() != 4 or mask.stride(3) != 1 or mask.shape[0] not in (1, B) or
+                mask.shape[1] not in (1, Hq) or mask.shape[2:] != (Sq, Sk)):
+            raise ValueError("mask must be [1|B, 1|Hq, Sq, Sk] float16 with a contiguous last dim")
+        p.mask = mask.data_ptr()
         p.m_sb = 0 if mask.shape[0] == 1 else mask.stride(0)
         p.m_sh = 0 if mask.shape[1] == 1 else mask.stride(1)
         p.m_ss = mask.stride(2)
     p.max_bias, p.softcap = max_bias, softcap
     dsinks = None
     if sinks is not None:
+        if sinks.dtype != torch.float32 or sinks.shape != (Hq,) or not sinks.is_contiguous():
+            raise ValueError("sinks must be a contiguous float32 tensor of shape [Hq]")
         dsinks = torch.empty_like(sinks)
-        p.sinks, p.gsinks = _ptr(sinks), _ptr(dsinks)
+        p.sinks, p.gsinks = sinks.data_ptr(), dsinks.data_ptr()
     lib = load()
     ref = ctypes.byref(p)
     if workspace is None:
@@ -599,9 +598,14 @@ def _dequant_entry(src, qtype, row_elems, out, kv_scale=1.0):
         raise ValueError("src rows must be contiguous")
     lead = src.shape[:-1]
     if out is None:
-        out = torch.empty(lead + (row_elems,), device=src.device, dtype=torch.bfloat16)
+        out = src.new_empty(lead + (row_elems,), dtype=torch.bfloat16)
     if out.dtype != torch.bfloat16 or out.shape[:-1] != lead or out.shape[-1] < row_elems or out.stride(-1) != 1:
         raise ValueError("out must be bf16 [..., >= row_elems] with the rows of src")
+    if src.is_contiguous() and out.is_contiguous() and src.dim() > 1 and src.shape[-1] > 0:
+        # one row stride each, without building the 2-D views (6 us of host time for two tensors)
+        width = src.shape[-1]
+        return KvDequantParams(src.data_ptr(), KV_QUANT[qtype][0], src.numel() // width, row_elems, width,
+                               out.data_ptr(), out.shape[-1], kv_scale), out
     s2, o2 = src.reshape(-1, src.shape[-1]), out.reshape(-1, out.shape[-1])
     if s2.data_ptr() != src.data_ptr() or o2.data_ptr() != out.data_ptr():
         raise ValueError("leading dimensions must collapse to one row stride")
@@ -743,14 +747,6 @@ def _check_pos(pos, B, S):
     return pos.stride(0) if pos.dim() == 2 and pos.shape[0] > 1 else 0
 
 
-def _rope_out(x, out):
-    if out is None:
-        return torch.empty_like(x, memory_format=torch.contiguous_format)
-    if out.shape != x.shape or out.dtype != x.dtype or out.stride(3) != 1:
-        raise ValueError("an output must have its input's shape and dtype and a contiguous last dim")
-    return out
-
-
 def rope(q, inv_freq, k=None, pos=None, pos0=0, interleaved=False, offset=0, inverse=False, mscale=1.0, out=None,
          k_out=None, stream=None):
     """Rotary positions (fa_rope): the pairs of columns [offset, offset + 2
@@ -761,33 +757,37 @@ def rope(q, inv_freq, k=None, pos=None, pos0=0, interleaved=False, offset=0, inv
     pos0 + s.  inverse=True turns back: the gradient.  out / k_out may be
     given, also as q / k themselves.  Returns (q turned, k turned or None)."""
     _need_current_device(q, k, pos, out, k_out)
-    for t in (q, k):
-        if t is not None and (t.dim() != 4 or t.stride(3) != 1 or t.dtype != q.dtype or
-                              t.dtype not in (torch.bfloat16, torch.float32)):
-            raise ValueError("q and k must be 4-D tensors of one dtype, bf16 or fp32, with a contiguous last dim")
-    if k is not None and (k.shape[0], k.shape[2], k.shape[3]) != (q.shape[0], q.shape[2], q.shape[3]):
-        raise ValueError("k must be [B, Hk, S, d] with q's B, S and d")
-    if k is None and k_out is not None:
-        raise ValueError("k_out without k")
+    dtype, qs = q.dtype, q.shape
+    if (dtype != torch.bfloat16 and dtype != torch.float32) or len(qs) != 4:
+        raise ValueError("q and k must be 4-D tensors of one dtype, bf16 or fp32")
+    B, Hq, S, d = qs
     _check_inv_freq(inv_freq)
-    B, Hq, S, d = q.shape
-    out = _rope_out(q, out)
-    p = RopeParams()
-    p.q, p.q_out = q.data_ptr(), out.data_ptr()
-    p.q_sb, p.q_sh, p.q_ss, _ = q.stride()
-    p.qo_sb, p.qo_sh, p.qo_ss, _ = out.stride()
-    p.B, p.Hq, p.S, p.d = B, Hq, S, d
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    q0, q1, q2, q3 = q.stride()
+    o0, o1, o2, o3 = out.stride()
+    if out.shape != qs or out.dtype != dtype or q3 != 1 or o3 != 1:
+        raise ValueError("an output must have its input's shape and dtype, and all a contiguous last dim")
+    p = RopeParams(q.data_ptr(), out.data_ptr(), q0, q1, q2, o0, o1, o2)
     if k is not None:
-        k_out = _rope_out(k, k_out)
-        p.k, p.k_out, p.Hk = _ptr(k), _ptr(k_out), k.shape[1]
-        p.k_sb, p.k_sh, p.k_ss, _ = k.stride()
-        p.ko_sb, p.ko_sh, p.ko_ss, _ = k_out.stride()
-    p.dtype = _odt(q.dtype)
+        ks = k.shape
+        if k.dtype != dtype or len(ks) != 4 or ks[0] != B or ks[2] != S or ks[3] != d:
+            raise ValueError("k must be [B, Hk, S, d] with q's dtype, B, S and d")
+        if k_out is None:
+            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+        q0, q1, q2, q3 = k.stride()
+        o0, o1, o2, o3 = k_out.stride()
+        if k_out.shape != ks or k_out.dtype != dtype or q3 != 1 or o3 != 1:
+            raise ValueError("an output must have its input's shape and dtype, and all a contiguous last dim")
+        p.k, p.k_out, p.Hk = k.data_ptr(), k_out.data_ptr(), ks[1]
+        p.k_sb, p.k_sh, p.k_ss, p.ko_sb, p.ko_sh, p.ko_ss = q0, q1, q2, o0, o1, o2
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    p.B, p.Hq, p.S, p.d, p.dtype = B, Hq, S, d, _odt(dtype)
     if pos is not None:
-        p.pos_sb = _check_pos(pos, B, S)
-        p.pos = _ptr(pos)
+        p.pos_sb, p.pos = _check_pos(pos, B, S), pos.data_ptr()
     p.pos0 = pos0
-    p.inv_freq, p.rot_dim, p.rot_offset = _ptr(inv_freq), 2 * inv_freq.numel(), offset
+    p.inv_freq, p.rot_dim, p.rot_offset = inv_freq.data_ptr(), 2 * inv_freq.numel(), offset
     p.interleaved, p.inverse, p.mscale = int(interleaved), int(inverse), mscale
     _check(load().fa_rope(ctypes.byref(p), _stream(stream)))
     return out, k_out
@@ -807,58 +807,55 @@ def kv_append(k, v, k_cache, v_cache, block_table, seq_lens, q_lens=None, inv_fr
     sequence; q [B,Hq,Sq,dk], if given, is turned too.  Returns q turned (in
     q_out, which may be q; rows past q_lens are zeros), or None without q."""
     _need_current_device(k, v, k_cache, v_cache, block_table, seq_lens, q_lens, q, q_out, pos)
-    for t in (k, v, q):
-        if t is not None and (t.dtype != torch.bfloat16 or t.dim() != 4 or t.stride(3) != 1):
-            raise ValueError("k, v and q must be 4-D bf16 with a contiguous last dim")
-    if k.shape[:3] != v.shape[:3]:
+    bf16, ks, vs, cs, cvs, ctype = torch.bfloat16, k.shape, v.shape, k_cache.shape, v_cache.shape, k_cache.dtype
+    k0, k1, k2, k3 = k.stride() if len(ks) == 4 else (0, 0, 0, 0)
+    v0, v1, v2, v3 = v.stride() if len(vs) == 4 else (0, 0, 0, 0)
+    if k.dtype != bf16 or v.dtype != bf16 or k3 != 1 or v3 != 1:
+        raise ValueError("k and v must be 4-D bf16 with a contiguous last dim")
+    B, Hkv, Sq, dk = ks
+    dv = vs[3]
+    if vs != (B, Hkv, Sq, dv):
         raise ValueError("k and v must have one B, Hkv and Sq")
-    B, Hkv, Sq, dk = k.shape
-    dv = v.shape[3]
-    cs, cvs, ctype = k_cache.shape, v_cache.shape, k_cache.dtype
-    if (len(cs) != 4 or len(cvs) != 4 or cs[1] != Hkv or cs[:3] != cvs[:3] or not k_cache.is_contiguous() or
-            not v_cache.is_contiguous()):
+    if len(cs) != 4 or cvs != (*cs[:3], cvs[-1]) or cs[1] != Hkv or not (k_cache.is_contiguous() and
+                                                                        v_cache.is_contiguous()):
         raise ValueError("the caches must be contiguous [num_blocks, Hkv, block_size, row] with k's Hkv")
-    if v_cache.dtype != ctype or ctype not in (torch.bfloat16, torch.uint8):
+    if v_cache.dtype != ctype or (ctype != bf16 and ctype != torch.uint8):
         raise ValueError("the caches must both be bf16, or both uint8 rows of a quantised type")
-    if ctype == torch.bfloat16 and (cs[3] != dk or cvs[3] != dv):
-        raise ValueError("the rows of a bf16 cache must be as wide as those of k and v")
-    p = KvAppendParams()
-    if ctype == torch.uint8:
-        kv_type, _ = _paged_kv(k, k_cache, kv_type)
-        per = KV_QUANT[kv_type][1]
-        if cs[3] != dk // 32 * per or cvs[3] != dv // 32 * per:
-            raise ValueError("the cache rows do not hold k's and v's rows as " + kv_type)
-        p.kv_type, p.k_scale, p.v_scale = KV_QUANT[kv_type][0], k_scale, v_scale
-    elif kv_type is not None:
-        raise ValueError("kv_type is for uint8 caches")
     for t, dim in ((block_table, 2), (seq_lens, 1), (q_lens, 1)):
         if t is not None and (t.dtype != torch.int32 or t.dim() != dim or t.shape[0] != B or not t.is_contiguous()):
             raise ValueError("block_table [B, max_blocks], seq_lens [B] and q_lens [B] must be contiguous int32")
-    p.k, p.v = k.data_ptr(), v.data_ptr()
-    p.k_sb, p.k_sh, p.k_ss, _ = k.stride()
-    p.v_sb, p.v_sh, p.v_ss, _ = v.stride()
-    p.k_cache, p.v_cache = k_cache.data_ptr(), v_cache.data_ptr()
-    p.block_table, p.seq_lens, p.q_lens = block_table.data_ptr(), seq_lens.data_ptr(), _ptr(q_lens)
-    p.max_blocks_per_seq = block_table.shape[1]
-    p.B, p.Hkv, p.Sq, p.dk, p.dv = B, Hkv, Sq, dk, dv
-    p.block_size, p.num_blocks = cs[2], cs[0]
+    p = KvAppendParams(k.data_ptr(), v.data_ptr(), k0, k1, k2, v0, v1, v2, k_cache.data_ptr(), v_cache.data_ptr(),
+                       block_table.data_ptr(), seq_lens.data_ptr(), _ptr(q_lens), block_table.shape[1], B, Hkv, Sq, dk,
+                       dv, cs[2], cs[0])
+    if ctype != bf16:
+        kv_type, _ = _paged_kv(k, k_cache, kv_type)
+        code, per = KV_QUANT[kv_type]
+        if cs[3] != dk // 32 * per or cvs[3] != dv // 32 * per:
+            raise ValueError("the cache rows do not hold k's and v's rows as " + kv_type)
+        p.kv_type, p.k_scale, p.v_scale = code, k_scale, v_scale
+    elif cs[3] != dk or cvs[3] != dv or kv_type is not None:
+        raise ValueError("the rows of a bf16 cache must be as wide as those of k and v (and kv_type is for uint8 ones)")
     p.mscale = mscale
     if inv_freq is not None:
         _check_inv_freq(inv_freq)
-        p.inv_freq, p.rot_dim, p.rot_offset = _ptr(inv_freq), 2 * inv_freq.numel(), offset
+        p.inv_freq, p.rot_dim, p.rot_offset = inv_freq.data_ptr(), 2 * inv_freq.numel(), offset
         p.interleaved = int(interleaved)
     if pos is not None:
-        p.pos_sb = _check_pos(pos, B, Sq)
-        p.pos = _ptr(pos)
+        p.pos_sb, p.pos = _check_pos(pos, B, Sq), pos.data_ptr()
     if q is not None:
         if inv_freq is None:
             raise ValueError("q without inv_freq: there is nothing to turn it by")
-        if (q.shape[0], q.shape[2], q.shape[3]) != (B, Sq, dk):
-            raise ValueError("q must be [B, Hq, Sq, dk] with k's B, Sq and dk")
-        q_out = _rope_out(q, q_out)
-        p.q, p.q_out, p.Hq = q.data_ptr(), q_out.data_ptr(), q.shape[1]
-        p.q_sb, p.q_sh, p.q_ss, _ = q.stride()
-        p.qo_sb, p.qo_sh, p.qo_ss, _ = q_out.stride()
+        qs = q.shape
+        if q.dtype != bf16 or len(qs) != 4 or qs[0] != B or qs[2] != Sq or qs[3] != dk:
+            raise ValueError("q must be bf16 [B, Hq, Sq, dk] with k's B, Sq and dk")
+        if q_out is None:
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        q0, q1, q2, q3 = q.stride()
+        o0, o1, o2, o3 = q_out.stride()
+        if q_out.shape != qs or q_out.dtype != bf16 or q3 != 1 or o3 != 1:
+            raise ValueError("q_out must have q's shape and dtype, and both a contiguous last dim")
+        p.q, p.q_out, p.Hq = q.data_ptr(), q_out.data_ptr(), qs[1]
+        p.q_sb, p.q_sh, p.q_ss, p.qo_sb, p.qo_sh, p.qo_ss = q0, q1, q2, o0, o1, o2
     elif q_out is not None:
         raise ValueError("q_out without q")
     _check(load().fa_kv_append(ctypes.byref(p), _stream(stream)))
