@@ -448,7 +448,7 @@ struct BwdWorker {
         const int shift = a.Sk - a.Sq;
         const bool capped = MODS && a.mods.softcap != 0.f;
         const bool masked = MODS && a.mods.mask != nullptr;
-        const float inv_cap = capped ? 1.f / (a.mods.softcap * kLog2e) : 0.f;
+        const float root = capped ? rsqrtf(a.mods.softcap) / kLog2e : 0.f;  // v root = sqrt(softcap) tanh
         float row_nlse = 0.f, row_ndelta = 0.f;
         if (!KV) {  // rows past Sq are padded in the workspace
             const int64_t r = ((int64_t)it.b * a.Hq + it.h) * a.pitch + xr;
@@ -473,11 +473,20 @@ struct BwdWorker {
                     const uint16_t *m = reinterpret_cast<const uint16_t *>(a.mods.mask) + (int64_t)it.b * a.mods.m_sb +
                                         (int64_t)hq * a.mods.m_sh;
                     if (KV) {
-                        m += min(xr, a.Sk - 1);
+                        m += min(xr, a.Sk - 1) + (int64_t)min(y0, a.Sq - 1) * a.mods.m_ss;
+                        if (y0 + 32 <= a.Sq) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            mk[i] = (uint32_t)__ldg(m + (int64_t)min(y0 + 2 * i, a.Sq - 1) * a.mods.m_ss) |
-                                    (uint32_t)__ldg(m + (int64_t)min(y0 + 2 * i + 1, a.Sq - 1) * a.mods.m_ss) << 16;
+                            for (int i = 0; i < 16; ++i, m += 2 * a.mods.m_ss)
+                                mk[i] = (uint32_t)__ldg(m) | (uint32_t)__ldg(m + a.mods.m_ss) << 16;
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                mk[i] = (uint32_t)__ldg(m);
+                                if (y0 + 2 * i + 1 < a.Sq) m += a.mods.m_ss;
+                                mk[i] |= (uint32_t)__ldg(m) << 16;
+                                if (y0 + 2 * i + 2 < a.Sq) m += a.mods.m_ss;
+                            }
+                        }
                     } else {
                         m += (int64_t)min(xr, a.Sq - 1) * a.mods.m_ss;
                         if (y0 + 32 <= a.Sk) {
@@ -533,11 +542,14 @@ struct BwdWorker {
                 }
                 if constexpr (MODS) {
                     if (capped) {
+                        // softcap (1 - tanh^2), as softcap - (v root)^2
                         softcap4(v, a.scale, a.mods.softcap);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float th = v[j] * inv_cap;
-                            cap[j] = fmaf(-th, th, 1.f) * a.mods.softcap;
+                        for (int j = 0; j < 4; j += 2) {
+                            const uint64_t w = f2_pack(v[j], v[j + 1]);
+                            f2_unpack(f2_fma(f2_mul(w, f2_pack(-root, -root)), f2_mul(w, f2_pack(root, root)),
+                                             f2_pack(a.mods.softcap, a.mods.softcap)),
+                                      cap[j], cap[j + 1]);
                         }
                     } else {
 #pragma unroll
@@ -547,8 +559,8 @@ struct BwdWorker {
 #pragma unroll
                         for (int j = 0; j < 4; j += 2) {
                             const float2 m = __half22float2(*reinterpret_cast<const __half2 *>(&mk[(i + j) / 2]));
-                            v[j] = fmaf(m.x, slope, v[j]);
-                            v[j + 1] = fmaf(m.y, slope, v[j + 1]);
+                            f2_unpack(f2_fma(f2_pack(m.x, m.y), f2_pack(slope, slope), f2_pack(v[j], v[j + 1])), v[j],
+                                      v[j + 1]);
                         }
                     }
                 }
@@ -562,7 +574,7 @@ struct BwdWorker {
                     x[k] = ex2(e0);
                     x[k + 1] = ex2(e1);
                     pk[k / 2] = pack_bf16x2(x[k], x[k + 1]);
-                    if (capped) x[k] *= cap[2 * j], x[k + 1] *= cap[2 * j + 1];
+                    if (capped) f2_unpack(f2_mul(f2_pack(x[k], x[k + 1]), f2_pack(cap[2 * j], cap[2 * j + 1])), x[k], x[k + 1]);
                 }
             }
             if (KV) {
@@ -716,15 +728,16 @@ bwd_tile_kernel(const __grid_constant__ CUtensorMap tmQx, const __grid_constant_
             }
             BwdProducer<CK> pk;
             BwdProducer<CQ> pq;
-            int ahead = atomicAdd(a.next, 1);
             bool kv = false;
             for (int k = 0;; ++k) {
-                const int i = ahead;
+                // Taken when the loads of the item before are all under way: its
+                // last tiles hide the counter's latency, and nothing is held
+                // by an SM that will not come to it soon.
+                const int i = atomicAdd(a.next, 1);
                 if (!c.wait1(2 + (k & 1), ((uint32_t)(k >> 1) & 1u) ^ 1u)) break;
                 slot[k & 1] = i;
                 mbar_arrive(c.bar(k & 1));
                 if (i >= a.items) break;
-                ahead = atomicAdd(a.next, 1);  // its latency passes under this item
                 if (i < a.kv_items) {
                     const BwdItem it = bwd_item<true, BN>(a, i);
                     kv = true;
