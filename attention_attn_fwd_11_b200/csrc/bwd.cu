@@ -710,6 +710,9 @@ bwd_tile_kernel(const __grid_constant__ CUtensorMap tmQx, const __grid_constant_
     __syncthreads();
     tc_fence_after();
     c.tmem = *tmem_holder;
+    // What follows reads the row kernel's results, or writes memory that
+    // earlier work on the stream may still read.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 
     // Item k of this CTA, or -1: waits until the producer has put it there.
     auto take = [&](int k) -> int {
@@ -847,6 +850,7 @@ template <int DV, bool O_BF16>
 __global__ void __launch_bounds__(256) bwd_prep_kernel(const PrepArgs a) {
     constexpr int LPR = DV / 8;                    // lanes of a row
     constexpr int N = kPrepRows * LPR / 256;       // rows of a thread
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.next = 0;
     if (a.blocks == 0) return;
     const int bh = (int)(blockIdx.x / (unsigned)a.blocks), r0 = (int)(blockIdx.x % (unsigned)a.blocks) * kPrepRows;
@@ -954,8 +958,18 @@ cudaError_t launch_tiles(const BwdLaunch &L, const BwdArgs &a, int num_sms, cuda
     }
     const int grid = a.items < num_sms ? a.items : num_sms;
     if (grid == 0) return cudaSuccess;
-    kern<<<grid, K::THREADS, K::SMEM_BYTES, stream>>>(L.tmQx, L.tmKx, L.tmVx, L.tmDOx, L.tmQy, L.tmKy, L.tmVy, L.tmDOy, a);
-    return cudaGetLastError();
+    // Starts under the row kernel's end and waits for it on the device.
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(K::THREADS);
+    cfg.dynamicSmemBytes = K::SMEM_BYTES;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, L.tmQx, L.tmKx, L.tmVx, L.tmDOx, L.tmQy, L.tmKy, L.tmVy, L.tmDOy, a);
 }
 
 }  // namespace
@@ -983,11 +997,6 @@ cudaError_t launch_bwd(const BwdLaunch &L, int num_sms, cudaStream_t stream) {
         cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    if (L.gsinks) {
-        bwd_sink_kernel<<<L.Hq, 512, 0, stream>>>(L.nlse2, L.ndelta, pitch, L.B, L.Hq, L.Sq, L.mods.sinks, L.gsinks);
-        cudaError_t e = cudaGetLastError();
-        if (e != cudaSuccess) return e;
-    }
     BwdArgs a = {};
     a.B = L.B, a.Hq = L.Hq, a.Hkv = L.Hkv, a.Sq = L.Sq, a.Sk = L.Sk, a.causal = L.causal;
     a.scale = L.scale, a.scale_log2 = L.scale * kLog2e;
@@ -1002,11 +1011,16 @@ cudaError_t launch_bwd(const BwdLaunch &L, int num_sms, cudaStream_t stream) {
     a.g_bf16 = L.g_bf16;
 #define FA_BWD_PAIR(DK_, DV_) \
     (L.has_mods ? launch_tiles<DK_, DV_, true>(L, a, num_sms, stream) : launch_tiles<DK_, DV_, false>(L, a, num_sms, stream))
-    if (L.dk == 64 && L.dv == 64) return FA_BWD_PAIR(64, 64);
-    if (L.dk == 128 && L.dv == 128) return FA_BWD_PAIR(128, 128);
-    if (L.dk == 192 && L.dv == 128) return FA_BWD_PAIR(192, 128);
+    cudaError_t e = cudaErrorInvalidValue;
+    if (L.dk == 64 && L.dv == 64) e = FA_BWD_PAIR(64, 64);
+    if (L.dk == 128 && L.dv == 128) e = FA_BWD_PAIR(128, 128);
+    if (L.dk == 192 && L.dv == 128) e = FA_BWD_PAIR(192, 128);
 #undef FA_BWD_PAIR
-    return cudaErrorInvalidValue;
+    if (e == cudaSuccess && L.gsinks) {
+        bwd_sink_kernel<<<L.Hq, 512, 0, stream>>>(L.nlse2, L.ndelta, pitch, L.B, L.Hq, L.Sq, L.mods.sinks, L.gsinks);
+        e = cudaGetLastError();
+    }
+    return e;
 }
 
 cudaError_t bwd_device_error(int clear, int *code) {
