@@ -11,21 +11,22 @@
 //   dQ_i   = scale sum_j dS_ij K_j,   dK_j = scale sum_i dS_ij Q_i
 //   dsink_h = -sum_i exp(sink_h - lse_i) D_i
 //
-// Three kernels on the caller's stream:
-//   1. bwd_prep_kernel: D and the LSE in base 2, one pass over O and dO.
-//      Rows with no visible key (LSE -inf) and the padding up to a whole
-//      128-row tile get LSE +inf, which makes every P of the row exactly 0.
-//   2. bwd_tile_kernel<..., true>: dK and dV.  A CTA owns 128 keys of one KV
-//      head and walks the query tiles of every head of its group, so the sum
-//      over the group's heads stays in its accumulators.
-//   3. bwd_tile_kernel<..., false>: dQ.  A CTA owns 128 queries of one head
-//      and walks the key tiles.
-// Scores and dO V^T are formed in both 2 and 3: seven matrix products where
-// five would do, but no sum crosses CTAs, so nothing is accumulated with
-// atomics in HBM and the result does not depend on timing.
+// Two kernels on the caller's stream (and a third for the sinks' gradient):
+//   1. bwd_prep_kernel: D and the LSE of every row, one pass over O and dO.
+//      Rows with no visible key (LSE -inf) and the padding up to a whole tile
+//      get LSE +inf, which makes every P of the row exactly 0.
+//   2. bwd_tile_kernel, persistent, in which every SM takes items from one
+//      list until it is empty:
+//      - 128 keys of one KV head, walking the query tiles of every head of its
+//        group: dK and dV, whose sums over the group's heads stay in the
+//        accumulators;
+//      - 128 queries of one head, walking the key tiles: dQ.
+// Scores and dO V^T are formed in both walks: seven matrix products where five
+// would do, but no sum crosses SMs, so nothing is accumulated with atomics in
+// HBM and the result does not depend on timing.
 //
-// Both walks are one kernel.  Its 128 resident rows X1, X2 (K and V; or Q and
-// dO) meet tiles of BN rows Y1, Y2 (Q and dO; or K and V):
+// Both walks are one code.  An item's 128 resident rows X1, X2 (K and V; or Q
+// and dO) meet tiles of BN rows Y1, Y2 (Q and dO; or K and V):
 //
 //   S = X1 Y1^T,  T = X2 Y2^T       (128 x BN each, fp32 in TMEM)
 //   A1 += dS Y1,  and for dK / dV A2 += P Y2
@@ -63,9 +64,9 @@ struct BwdArgs {
     int B, Hq, Hkv, Sq, Sk, causal;
     float scale, scale_log2;
     ScoreMods mods;
-    const float *nlse2, *ndelta;  // -LSE in base 2 and -D of every row
-    const uint4 *ext;             // the two of a row as the B side of the extra step (see BwdCfg)
-    int64_t pitch;                // rows per (batch, head) of the three
+    const float *nlse, *ndelta;  // -LSE and -D of every row
+    const uint4 *ext;            // the two of a row as the B side of the extra step (see BwdCfg)
+    int64_t pitch;               // rows per (batch, head) of the three
     int kv_items, items;          // 128-key tiles of every KV head, then 128-query tiles of every head
     int *next;                    // first item that no CTA has taken
     BwdGrad gq, gk, gv;
@@ -230,7 +231,7 @@ struct BwdProducer {
                 if (C::EXT) {
                     bulk_load(sr, a.ext + row, C::BN * 16, f1);
                 } else {
-                    bulk_load(sr, a.nlse2 + row, C::BN * 4, f1);
+                    bulk_load(sr, a.nlse + row, C::BN * 4, f1);
                     bulk_load(sr + C::BN * 4, a.ndelta + row, C::BN * 4, f1);
                 }
             }
@@ -452,7 +453,7 @@ struct BwdWorker {
         float row_nlse = 0.f, row_ndelta = 0.f;
         if (!KV) {  // rows past Sq are padded in the workspace
             const int64_t r = ((int64_t)it.b * a.Hq + it.h) * a.pitch + xr;
-            row_nlse = __ldg(a.nlse2 + r);
+            row_nlse = __ldg(a.nlse + r) * (MODS ? 1.f : kLog2e);
             row_ndelta = __ldg(a.ndelta + r);
         }
         // dQ: columns c >= lim_hi - y0 of this row are hidden; dK / dV:
@@ -504,7 +505,7 @@ struct BwdWorker {
                     }
                 }
             }
-            const float slope = MODS ? alibi_slope(a.mods, hq) * kLog2e : 0.f;
+            const float slope = MODS ? alibi_slope(a.mods, hq) : 0.f;
             if (KV && MODS && !c.wait(bars + C::FULL1 + r1.s, r1.ph)) return false;
             if (!c.wait(bars + B_SFULL, tiles & 1u)) return false;
             tc_fence_after();
@@ -531,7 +532,10 @@ struct BwdWorker {
             for (int i = 0; i < 32; i += 4) {
                 float v[4] = {x[i], x[i + 1], x[i + 2], x[i + 3]};
                 float cap[4] = {1.f, 1.f, 1.f, 1.f};
-                uint64_t nl[2];  // -LSE of the four, in base 2
+                // -LSE of the four: natural with modifiers, where the mask is
+                // added to it first (both may be as large as the mask's lowest
+                // value, and their sum is what counts), else in base 2
+                uint64_t nl[2];
                 if (C::EXT) {
                     nl[0] = nl[1] = 0;
                 } else if (KV) {
@@ -559,8 +563,7 @@ struct BwdWorker {
 #pragma unroll
                         for (int j = 0; j < 4; j += 2) {
                             const float2 m = __half22float2(*reinterpret_cast<const __half2 *>(&mk[(i + j) / 2]));
-                            f2_unpack(f2_fma(f2_pack(m.x, m.y), f2_pack(slope, slope), f2_pack(v[j], v[j + 1])), v[j],
-                                      v[j + 1]);
+                            nl[j / 2] = f2_fma(f2_pack(m.x, m.y), f2_pack(slope, slope), nl[j / 2]);
                         }
                     }
                 }
@@ -570,7 +573,9 @@ struct BwdWorker {
                     const int k = i + 2 * j;
                     const uint64_t xx = f2_pack(v[2 * j], v[2 * j + 1]);
                     float e0, e1;
-                    f2_unpack(C::EXT ? f2_mul(xx, sc2) : MODS ? f2_add(xx, nl[j]) : f2_fma(xx, sc2, nl[j]), e0, e1);
+                    f2_unpack(C::EXT ? f2_mul(xx, sc2)
+                              : MODS ? f2_fma(nl[j], f2_pack(kLog2e, kLog2e), xx)
+                                     : f2_fma(xx, sc2, nl[j]), e0, e1);
                     x[k] = ex2(e0);
                     x[k + 1] = ex2(e1);
                     pk[k / 2] = pack_bf16x2(x[k], x[k + 1]);
@@ -819,7 +824,7 @@ struct PrepArgs {
     int64_t o_sb, o_sh, o_ss, do_sb, do_sh, do_ss;
     int Hq, Sq, o_bf16;
     int blocks;  // of kPrepRows rows, for each head
-    float *nlse2, *ndelta;
+    float *nlse, *ndelta;
     uint4 *ext;  // NULL: not wanted
     float inv_scale;
     int *next;  // set to 0
@@ -905,7 +910,7 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const PrepArgs a) {
         } else {
             d = 0.f;
         }
-        a.nlse2[r] = -lse * kLog2e;
+        a.nlse[r] = -lse;
         a.ndelta[r] = -d;
         if (a.ext) {
             // In units of q.k; a row that sees nothing gets bf16's lowest
@@ -920,15 +925,15 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const PrepArgs a) {
 }
 
 // dsink_h: one block a head, rows in a fixed order.
-__global__ void __launch_bounds__(512) bwd_sink_kernel(const float *nlse2, const float *ndelta, int64_t pitch, int B,
+__global__ void __launch_bounds__(512) bwd_sink_kernel(const float *nlse, const float *ndelta, int64_t pitch, int B,
                                                        int Hq, int Sq, const float *sinks, float *out) {
     __shared__ float part[16];
     const int h = blockIdx.x;
-    const float sk = sinks[h] * kLog2e;
+    const float sk = sinks[h];
     float acc = 0.f;
     for (int b = 0; b < B; ++b) {
         const int64_t r = ((int64_t)b * Hq + h) * pitch;
-        for (int i = threadIdx.x; i < Sq; i += 512) acc += ex2(sk + nlse2[r + i]) * ndelta[r + i];
+        for (int i = threadIdx.x; i < Sq; i += 512) acc += ex2((sk + nlse[r + i]) * kLog2e) * ndelta[r + i];
     }
 #pragma unroll
     for (int k = 16; k > 0; k >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, k);
@@ -983,7 +988,7 @@ cudaError_t launch_bwd(const BwdLaunch &L, int num_sms, cudaStream_t stream) {
         p.do_sb = L.do_sb, p.do_sh = L.do_sh, p.do_ss = L.do_ss;
         p.Hq = L.Hq, p.Sq = L.Sq;
         p.blocks = (int)(pitch / kPrepRows);
-        p.nlse2 = L.nlse2, p.ndelta = L.ndelta;
+        p.nlse = L.nlse, p.ndelta = L.ndelta;
         p.ext = L.has_mods ? nullptr : static_cast<uint4 *>(L.ext), p.inv_scale = 1.f / L.scale;
         p.next = L.next;
         unsigned grid = (unsigned)(L.B * L.Hq) * (unsigned)p.blocks;
@@ -1001,7 +1006,7 @@ cudaError_t launch_bwd(const BwdLaunch &L, int num_sms, cudaStream_t stream) {
     a.B = L.B, a.Hq = L.Hq, a.Hkv = L.Hkv, a.Sq = L.Sq, a.Sk = L.Sk, a.causal = L.causal;
     a.scale = L.scale, a.scale_log2 = L.scale * kLog2e;
     a.mods = L.mods;
-    a.nlse2 = L.nlse2, a.ndelta = L.ndelta, a.ext = static_cast<const uint4 *>(L.ext), a.pitch = pitch;
+    a.nlse = L.nlse, a.ndelta = L.ndelta, a.ext = static_cast<const uint4 *>(L.ext), a.pitch = pitch;
     a.kv_items = L.B * L.Hkv * ((L.Sk + 127) / 128);
     a.items = a.kv_items + L.B * L.Hq * ((L.Sq + 127) / 128);
     a.next = L.next;
@@ -1017,7 +1022,7 @@ cudaError_t launch_bwd(const BwdLaunch &L, int num_sms, cudaStream_t stream) {
     if (L.dk == 192 && L.dv == 128) e = FA_BWD_PAIR(192, 128);
 #undef FA_BWD_PAIR
     if (e == cudaSuccess && L.gsinks) {
-        bwd_sink_kernel<<<L.Hq, 512, 0, stream>>>(L.nlse2, L.ndelta, pitch, L.B, L.Hq, L.Sq, L.mods.sinks, L.gsinks);
+        bwd_sink_kernel<<<L.Hq, 512, 0, stream>>>(L.nlse, L.ndelta, pitch, L.B, L.Hq, L.Sq, L.mods.sinks, L.gsinks);
         e = cudaGetLastError();
     }
     return e;

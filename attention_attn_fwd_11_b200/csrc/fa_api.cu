@@ -925,6 +925,8 @@ fa_status fa_rope(const fa_rope_params *p, void *stream) {
     if (p->dtype != FA_F32 && p->dtype != FA_BF16) return fail(FA_ERR_INVALID_ARG, "fa_rope: dtype");
     if (!p->inv_freq) return fail(FA_ERR_INVALID_ARG, "fa_rope: inv_freq is NULL");
     if ((uintptr_t)p->pos & 3u) return fail(FA_ERR_INVALID_ARG, "fa_rope: pos must be 4-byte aligned");
+    if (!p->pos && (int64_t)p->pos0 + p->S > 0x7fffffffLL)
+        return fail(FA_ERR_INVALID_ARG, "fa_rope: pos0 + S must be < 2^31");
     if ((p->k || p->k_out) && p->Hk == 0) return fail(FA_ERR_INVALID_ARG, "fa_rope: k needs Hk > 0");
     fa::RopeLaunch L;
     memset(&L, 0, sizeof L);
@@ -968,8 +970,9 @@ fa_status fa_kv_append(const fa_kv_append_params *p, void *stream) {
         return fail(FA_ERR_UNSUPPORTED,
                     "fa_kv_append: dk and dv must be multiples of 16 up to 1024, 128 for quantised caches (got %d/%d)",
                     p->dk, p->dv);
-    if (p->kv_type == FA_KV_FP8_E4M3 && (!finite_pos(p->k_scale) || !finite_pos(p->v_scale)))
-        return fail(FA_ERR_INVALID_ARG, "fa_kv_append: k_scale and v_scale must be finite and > 0");
+    if (p->kv_type == FA_KV_FP8_E4M3 && (!finite_pos(p->k_scale) || !finite_pos(p->v_scale) ||
+                                         !isfinite(1.f / p->k_scale) || !isfinite(1.f / p->v_scale)))
+        return fail(FA_ERR_INVALID_ARG, "fa_kv_append: k_scale, v_scale and their reciprocals must be finite and > 0");
     const int Hq = p->q || p->q_out ? p->Hq : 0;
     if ((p->q || p->q_out) && (p->Hq <= 0 || !p->inv_freq))
         return fail(FA_ERR_INVALID_ARG, "fa_kv_append: q needs Hq > 0 and inv_freq");
@@ -1133,7 +1136,7 @@ fa_status fa_bwd(const fa_bwd_params *p, void *stream) {
     }
     L.has_mods = p->mask || p->softcap > 0.f || p->scale < 1e-30f;
     L.gsinks = p->gsinks;
-    L.nlse2 = static_cast<float *>(p->workspace);
+    L.nlse = static_cast<float *>(p->workspace);
     L.ndelta = reinterpret_cast<float *>(static_cast<char *>(p->workspace) + each);
     L.ext = static_cast<char *>(p->workspace) + 2 * each;
     L.next = reinterpret_cast<int *>(static_cast<char *>(p->workspace) + 6 * each);

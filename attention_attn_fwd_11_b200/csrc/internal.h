@@ -210,11 +210,11 @@ struct BwdLaunch {
     // for scales below 1e-30, whose LSE / scale may leave fp32's range.
     bool has_mods;
     float *gsinks;   // NULL: not asked for
-    float *nlse2, *ndelta;  // workspace: [B * Hq, bwd_pitch(Sq)] each,
+    float *nlse, *ndelta;  // workspace: [B * Hq, bwd_pitch(Sq)] each,
     void *ext;              // and as many 16-byte rows,
     int *next;              // and the counter from which CTAs take their tiles
 };
-// Rows of nlse2 and ndelta per (batch, head): Sq rounded up to whole tiles,
+// Rows of nlse and ndelta per (batch, head): Sq rounded up to whole tiles,
 // walked (128 or 96) and the resident one (128) alike.
 inline int64_t bwd_pitch(int Sq) { return ((int64_t)Sq + 383) / 384 * 384; }
 // Rows of a walked tile: 128, or what TMEM holds beside 192 + 128 columns of

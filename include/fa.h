@@ -507,7 +507,7 @@ fa_status fa_decode_gather(const fa_decode_gather_params *p, void *stream);
  *   Columns [rot_offset, rot_offset + rot_dim) are rotated, the others are
  *     copied (left alone where the output is the input).  Pair i is columns
  *     (i, i + rot_dim / 2) of them, or with interleaved != 0 (2i, 2i + 1).
- *   pos: NULL (row s is at position pos0 + s) or int32, the position of row s
+ *   pos: NULL (row s is at position pos0 + s < 2^31) or int32, the position of row s
  *     of batch entry b at b * pos_sb + s (pos_sb 0 broadcasts); may be
  *     negative.
  * Requirements: d, rot_dim and rot_offset multiples of 16, d <= 1024,
@@ -581,7 +581,7 @@ typedef struct {
     int max_blocks_per_seq;
     int B, Hkv, Sq, dk, dv, block_size, num_blocks;
     int kv_type; /* fa_kv_quant */
-    float k_scale, v_scale; /* FA_KV_FP8_E4M3: finite and > 0 */
+    float k_scale, v_scale; /* FA_KV_FP8_E4M3: finite and > 0, as their reciprocals */
     const double *inv_freq; /* host, or NULL */
     int rot_dim, rot_offset, interleaved;
     float mscale;

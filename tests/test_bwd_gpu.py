@@ -179,6 +179,16 @@ def test_modifiers(dk, dv, causal):
 
 
 @pytest.mark.parametrize("dk,dv", PAIRS)
+@pytest.mark.parametrize("lowest", [-65504.0, -30000.0])
+def test_rows_whose_mask_is_the_lowest_value_everywhere(dk, dv, lowest):
+    """Such rows are not empty: their weights follow from the scores, although scores and LSE sit at the mask's value."""
+    mask = torch.zeros((2, 1, 150, 264), device="cuda")
+    mask[:, :, 7::13] = lowest
+    mask[1, :, 100:] = lowest
+    run(2, 4, 2, 150, 261, dk, dv, False, seed=6, mask=mask.half()[..., :261], grad_dtype=torch.float32)
+
+
+@pytest.mark.parametrize("dk,dv", PAIRS)
 @pytest.mark.parametrize("S", [128, 256, 300])
 @pytest.mark.parametrize("causal", [False, True])
 def test_many_short_walks(dk, dv, S, causal):

@@ -72,6 +72,7 @@ ROPE = dict(q=16, q_out=32, q_sb=2048, q_sh=1024, q_ss=128, qo_sb=2048, qo_sh=10
     (dict(q_ss=132), fa.FA_ERR_INVALID_ARG), (dict(qo_ss=0), fa.FA_ERR_INVALID_ARG),
     (dict(qo_sh=0), fa.FA_ERR_INVALID_ARG), (dict(q_out=16, qo_ss=256), fa.FA_ERR_INVALID_ARG),
     (dict(pos=2), fa.FA_ERR_INVALID_ARG), (dict(k=16), fa.FA_ERR_INVALID_ARG), (dict(Hk=2), fa.FA_ERR_INVALID_ARG),
+    (dict(pos0=(1 << 31) - 8), fa.FA_ERR_INVALID_ARG),
     (dict(B=1 << 16, S=1 << 15), fa.FA_ERR_INVALID_ARG), (dict(Hq=65536), fa.FA_ERR_INVALID_ARG),
     (dict(B=0, q=0, q_out=0), fa.FA_OK), (dict(S=0), fa.FA_OK)])
 def test_rope_refused(kw, status):
@@ -90,6 +91,7 @@ APPEND = dict(k=16, v=32, k_sb=2048, k_sh=1024, k_ss=128, v_sb=2048, v_sh=1024, 
     (dict(dk=64, rot_dim=64, kv_type=fa.FA_KV_Q8_0), fa.FA_ERR_UNSUPPORTED),
     (dict(kv_type=fa.FA_KV_FP8_E4M3), fa.FA_ERR_INVALID_ARG),
     (dict(kv_type=fa.FA_KV_FP8_E4M3, k_scale=1.0, v_scale=-1.0), fa.FA_ERR_INVALID_ARG),
+    (dict(kv_type=fa.FA_KV_FP8_E4M3, k_scale=1e-40, v_scale=1.0), fa.FA_ERR_INVALID_ARG),
     (dict(kv_type=fa.FA_KV_Q8_0, rot_dim=96), fa.FA_ERR_UNSUPPORTED),
     (dict(kv_type=fa.FA_KV_Q4_0, rot_dim=48, interleaved=1), fa.FA_ERR_UNSUPPORTED),
     (dict(kv_type=fa.FA_KV_Q8_0, rot_dim=64, rot_offset=16), fa.FA_ERR_UNSUPPORTED),
