@@ -229,20 +229,30 @@ struct Coder {
         inv = ok ? 1.f / d : 0.f;
         half = 0.5f * fabsf(d);
     }
-    // The code in the low bits (two's complement).
-    FA_DEV uint32_t operator()(float x) const {
+    // The codes of a vector, each in the low bits (two's complement).
+    FA_DEV void operator()(const float (&x)[8], uint32_t (&q)[8]) const {
         constexpr float magic = 12582912.f;
-        float r = fminf(fmaxf(x * inv, lo), hi) + magic;
-        float n = r - magic;
-        const float e = fmaf(-n, d, x);
-        if (fabsf(e) >= half && ok) {
-            const float t = d < 0.f ? -e : e;
-            const bool odd = __float_as_uint(r) & 1u;
-            if (t > half || (t == half && odd)) n += 1.f;
-            if (t < -half || (t == -half && odd)) n -= 1.f;
-            r = fminf(fmaxf(n, lo), hi) + magic;
+        float r[8], e[8];
+        bool near = false;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            r[j] = fminf(fmaxf(x[j] * inv, lo), hi) + magic;
+            e[j] = fmaf(magic - r[j], d, x[j]);
+            near |= fabsf(e[j]) >= half;
         }
-        return ok ? __float_as_uint(r) : 0u;
+        if (near) {  // rare: a quotient next to a half, or beyond the codes
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float t = d < 0.f ? -e[j] : e[j];
+                const bool odd = __float_as_uint(r[j]) & 1u;
+                float n = r[j] - magic;
+                if (t > half || (t == half && odd)) n += 1.f;
+                if (t < -half || (t == -half && odd)) n -= 1.f;
+                r[j] = fminf(fmaxf(n, lo), hi) + magic;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) q[j] = ok ? __float_as_uint(r[j]) : 0u;
     }
 };
 
@@ -288,11 +298,13 @@ FA_DEV void put(uint8_t *dst, int c0, int c1, bool split, float inv, const float
             uint8_t *blk = dst + (c >> 5) * 34;
             const int part = (c >> 3) & 3;
             if (live && part == 0) *reinterpret_cast<__half *>(blk) = h;
+            uint32_t q[8];
+            code(v ? y : x, q);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t q0 = code(v ? y[2 * j] : x[2 * j]), q1 = code(v ? y[2 * j + 1] : x[2 * j + 1]);
-                if (live) reinterpret_cast<uint16_t *>(blk + 2 + 8 * part)[j] = (uint16_t)__byte_perm(q0, q1, 0x0040);
-            }
+            for (int j = 0; j < 4; ++j)
+                if (live)
+                    reinterpret_cast<uint16_t *>(blk + 2 + 8 * part)[j] =
+                        (uint16_t)__byte_perm(q[2 * j], q[2 * j + 1], 0x0040);
         }
     } else {
         // q4_0.  The key orders by magnitude, then the lowest index, and
@@ -315,9 +327,11 @@ FA_DEV void put(uint8_t *dst, int c0, int c1, bool split, float inv, const float
             const float m = __uint_as_float((uint32_t)(k >> 32) | (uint32_t)(k & 1) << 31);
             h[v] = block_scale(m / -8.f);
             const Coder code(__half2float(h[v]), -8.f, 7.f);
+            uint32_t q[8];
+            code(v ? y : x, q);
             n[v] = 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) n[v] |= ((code(v ? y[j] : x[j]) + 8u) & 15u) << (4 * j);
+            for (int j = 0; j < 8; ++j) n[v] |= ((q[j] + 8u) & 15u) << (4 * j);
         }
         // Byte j of a block holds values j (low) and j + 16 (high): vectors 0
         // and 2, or 1 and 3, of the block.  Split: lanes 0, 1 of four own the
