@@ -465,46 +465,48 @@ struct BwdWorker {
         for (int t = 0; t < it.n; ++t) {
             const int y0 = (it.y_first + y) * BN + wg * 32;  // first column: query or key
             const float *sl = reinterpret_cast<const float *>(c.smem + C::OFF_ROW + r1.s * C::ROW_BYTES) + wg * 32;
-            // The tile's mask values (f16 pairs), asked for before its scores
-            // are waited for.  Rows and keys past the end read the last one's:
+            // Mask values (f16 pairs) of 16 of the columns: the first half asked
+            // for before the scores are waited for, the second under the first
+            // half's work.  Rows and keys past the end read the last one's:
             // their P is 0, or their results are not stored.
-            [[maybe_unused]] uint32_t mk[16];
-            if constexpr (MODS) {
-                if (masked) {
-                    const uint16_t *m = reinterpret_cast<const uint16_t *>(a.mods.mask) + (int64_t)it.b * a.mods.m_sb +
-                                        (int64_t)hq * a.mods.m_sh;
-                    if (KV) {
-                        m += min(xr, a.Sk - 1) + (int64_t)min(y0, a.Sq - 1) * a.mods.m_ss;
-                        if (y0 + 32 <= a.Sq) {
+            [[maybe_unused]] uint32_t mk[2][8];
+            const auto load_mask = [&](int half) {
+                const int f = y0 + 16 * half;
+                const uint16_t *m = reinterpret_cast<const uint16_t *>(a.mods.mask) + (int64_t)it.b * a.mods.m_sb +
+                                    (int64_t)hq * a.mods.m_sh;
+                if (KV) {
+                    m += min(xr, a.Sk - 1) + (int64_t)min(f, a.Sq - 1) * a.mods.m_ss;
+                    if (f + 16 <= a.Sq) {
 #pragma unroll
-                            for (int i = 0; i < 16; ++i, m += 2 * a.mods.m_ss)
-                                mk[i] = (uint32_t)__ldg(m) | (uint32_t)__ldg(m + a.mods.m_ss) << 16;
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                mk[i] = (uint32_t)__ldg(m);
-                                if (y0 + 2 * i + 1 < a.Sq) m += a.mods.m_ss;
-                                mk[i] |= (uint32_t)__ldg(m) << 16;
-                                if (y0 + 2 * i + 2 < a.Sq) m += a.mods.m_ss;
-                            }
-                        }
+                        for (int i = 0; i < 8; ++i, m += 2 * a.mods.m_ss)
+                            mk[half][i] = (uint32_t)__ldg(m) | (uint32_t)__ldg(m + a.mods.m_ss) << 16;
                     } else {
-                        m += (int64_t)min(xr, a.Sq - 1) * a.mods.m_ss;
-                        if (y0 + 32 <= a.Sk) {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const uint4 w = __ldg(reinterpret_cast<const uint4 *>(m + y0) + i);
-                                mk[4 * i] = w.x, mk[4 * i + 1] = w.y, mk[4 * i + 2] = w.z, mk[4 * i + 3] = w.w;
-                            }
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                mk[i] = (uint32_t)__ldg(m + min(y0 + 2 * i, a.Sk - 1)) |
-                                        (uint32_t)__ldg(m + min(y0 + 2 * i + 1, a.Sk - 1)) << 16;
+                        for (int i = 0; i < 8; ++i) {
+                            mk[half][i] = (uint32_t)__ldg(m);
+                            if (f + 2 * i + 1 < a.Sq) m += a.mods.m_ss;
+                            mk[half][i] |= (uint32_t)__ldg(m) << 16;
+                            if (f + 2 * i + 2 < a.Sq) m += a.mods.m_ss;
                         }
                     }
+                } else {
+                    m += (int64_t)min(xr, a.Sq - 1) * a.mods.m_ss;
+                    if (f + 16 <= a.Sk) {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const uint4 w = __ldg(reinterpret_cast<const uint4 *>(m + f) + i);
+                            mk[half][4 * i] = w.x, mk[half][4 * i + 1] = w.y;
+                            mk[half][4 * i + 2] = w.z, mk[half][4 * i + 3] = w.w;
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            mk[half][i] = (uint32_t)__ldg(m + min(f + 2 * i, a.Sk - 1)) |
+                                          (uint32_t)__ldg(m + min(f + 2 * i + 1, a.Sk - 1)) << 16;
+                    }
                 }
-            }
+            };
+            if (MODS && masked) load_mask(0);
             const float slope = MODS ? alibi_slope(a.mods, hq) : 0.f;
             if (KV && MODS && !c.wait(bars + C::FULL1 + r1.s, r1.ph)) return false;
             if (!c.wait(bars + B_SFULL, tiles & 1u)) return false;
@@ -530,6 +532,7 @@ struct BwdWorker {
             uint32_t pk[16];
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
+                if (MODS && masked && i == 0) load_mask(1);
                 float v[4] = {x[i], x[i + 1], x[i + 2], x[i + 3]};
                 float cap[4] = {1.f, 1.f, 1.f, 1.f};
                 // -LSE of the four: natural with modifiers, where the mask is
@@ -562,7 +565,7 @@ struct BwdWorker {
                     if (masked) {
 #pragma unroll
                         for (int j = 0; j < 4; j += 2) {
-                            const float2 m = __half22float2(*reinterpret_cast<const __half2 *>(&mk[(i + j) / 2]));
+                            const float2 m = __half22float2(*reinterpret_cast<const __half2 *>(&mk[i / 16][(i + j) % 16 / 2]));
                             nl[j / 2] = f2_fma(f2_pack(m.x, m.y), f2_pack(slope, slope), nl[j / 2]);
                         }
                     }
@@ -785,23 +788,26 @@ bwd_tile_kernel(const __grid_constant__ CUtensorMap tmQx, const __grid_constant_
         mbar_wait_drain(c.bar(K::BAR_END), 0);
         __syncwarp();
     } else if (warp >= 4) {
-        BwdWorker<DK, DV, true, MODS, CK> wk;
-        BwdWorker<DK, DV, false, MODS, CQ> wq;
+        // All of dK / dV, then all of dQ (the list's order).
         uint32_t dones = 0;
-        bool kv = false;
-        for (int k = 0, i; (i = take(k)) >= 0; ++k) {
-            if (i < a.kv_items) {
-                kv = true;
-                if (!wk.item(c, a, bwd_item<true, BN>(a, i), K::BAR_KV, K::BAR_DONE, dones)) break;
-            } else {
-                if (kv) {
-                    // dQ's dS may lie where dK and dV were: every warp must have read them.
-                    wq.arrive(c, K::BAR_MOVED, lane);
-                    if (!c.wait(K::BAR_MOVED, 0)) break;
-                    kv = false;
-                }
-                if (!wq.item(c, a, bwd_item<false, BN>(a, i), K::BAR_Q, K::BAR_DONE, dones)) break;
+        int k = 0, i = take(0);
+        bool ok = true;
+        if (i >= 0 && i < a.kv_items) {
+            BwdWorker<DK, DV, true, MODS, CK> w;
+            while (ok && i >= 0 && i < a.kv_items) {
+                ok = w.item(c, a, bwd_item<true, BN>(a, i), K::BAR_KV, K::BAR_DONE, dones);
+                if (ok) i = take(++k);
             }
+            // dQ's dS may lie where dK and dV were: every warp must have read them.
+            if (ok && i >= 0) {
+                w.arrive(c, K::BAR_MOVED, lane);
+                ok = c.wait(K::BAR_MOVED, 0);
+            }
+        }
+        BwdWorker<DK, DV, false, MODS, CQ> w;
+        while (ok && i >= 0) {
+            ok = w.item(c, a, bwd_item<false, BN>(a, i), K::BAR_Q, K::BAR_DONE, dones);
+            if (ok) i = take(++k);
         }
     }
 
