@@ -188,7 +188,7 @@ struct BwdCta {
     volatile int *abort_flag;
     FA_DEV uint32_t bar(int i) const { return bar0 + 8u * (uint32_t)i; }
     FA_DEV bool wait(int i, uint32_t parity) const {
-        return mbar_wait_warp_fast(bar(i), parity, abort_flag, &g_bwd_err);
+        return mbar_wait_warp(bar(i), parity, abort_flag, &g_bwd_err);
     }
     FA_DEV bool wait1(int i, uint32_t parity) const { return mbar_wait(bar(i), parity, abort_flag, &g_bwd_err); }
 };

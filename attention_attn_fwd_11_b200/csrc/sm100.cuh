@@ -448,16 +448,6 @@ FA_DEV bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int *abort_fl
     return __all_sync(0xffffffffu, r);
 }
 
-// The same for waits that decide a kernel's pace: the clock that bounds the
-// wait is read only after a number of tries.  Reading it up front delays a
-// waiter whose barrier completes a moment later by some 300 cycles.
-FA_DEV bool mbar_wait_warp_fast(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *err) {
-#pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-    return mbar_wait_warp(bar, parity, abort_flag, err);
-}
-
 // Instruction descriptor for kind::f16 with bf16 A/B and fp32 D.
 // a_mn / b_mn select MN-major (transposed) operands.
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool a_mn, bool b_mn) {
