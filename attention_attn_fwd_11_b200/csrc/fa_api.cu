@@ -10,6 +10,7 @@
 #include <string.h>
 
 #include <mutex>
+#include <utility>
 
 #include "../../include/fa.h"
 #include "internal.h"
@@ -404,11 +405,25 @@ size_t bwd_row_bytes(const fa_bwd_params *p) {  // of the row LSE, of D, and a q
 }
 
 // A gradient's strides: vector stores of 16 bytes, rows that do not overlap.
-fa_status check_grad(const char *name, const void *g, int64_t sb, int64_t sh, int64_t ss, int d, int unit) {
+// Dimensions of extent 1 may have any stride.
+fa_status check_grad(const char *name, const void *g, int64_t sb, int64_t sh, int64_t ss, int B, int H, int S, int d,
+                     int unit) {
     if (!g || !aligned16(g)) return fail(FA_ERR_INVALID_ARG, "fa_bwd: %s is NULL or not 16-byte aligned", name);
-    if (sb % unit || sh % unit || ss % unit || ss < d)
-        return fail(FA_ERR_INVALID_ARG, "fa_bwd: %s strides must be multiples of %d elements, rows >= the width", name,
-                    unit);
+    int64_t st[3] = {sb, sh, ss}, n[3] = {B, H, S};
+    int64_t span = d;  // elements from the first to the last of the dimensions looked at
+    for (int i = 0; i < 3; ++i) {
+        for (int j = i + 1; j < 3; ++j)  // extents of 1 first, then by stride
+            if (n[i] > 1 && (n[j] == 1 || st[j] < st[i])) {
+                std::swap(st[i], st[j]);
+                std::swap(n[i], n[j]);
+            }
+        if (n[i] == 1) continue;
+        if (st[i] % unit)
+            return fail(FA_ERR_INVALID_ARG, "fa_bwd: %s strides must be multiples of %d elements", name, unit);
+        if (st[i] < span) return fail(FA_ERR_INVALID_ARG, "fa_bwd: the rows of %s overlap", name);
+        if (st[i] > (int64_t(1) << 40)) return fail(FA_ERR_INVALID_ARG, "fa_bwd: %s strides out of range", name);
+        span += (n[i] - 1) * st[i];
+    }
     return FA_OK;
 }
 
@@ -1049,16 +1064,27 @@ fa_status fa_bwd(const fa_bwd_params *p, void *stream) {
         if (!p->q || !p->o || !p->dout || !p->lse || !aligned16(p->q) || !aligned16(p->o) || !aligned16(p->dout))
             return fail(FA_ERR_INVALID_ARG, "fa_bwd: q, o, dout, lse must be given, tensors 16-byte aligned");
         const int ovec = p->o_dtype == FA_F32 ? 4 : 8;
-        if (p->o_ss % ovec || p->o_sh % ovec || p->o_sb % ovec)
+        if ((p->Sq > 1 && p->o_ss % ovec) || (p->Hq > 1 && p->o_sh % ovec) || (p->B > 1 && p->o_sb % ovec))
             return fail(FA_ERR_INVALID_ARG, "fa_bwd: o strides must be multiples of %d elements", ovec);
     }
     if (keys && (!p->k || !p->v || !aligned16(p->k) || !aligned16(p->v)))
         return fail(FA_ERR_INVALID_ARG, "fa_bwd: k and v must be given, 16-byte aligned");
     const int gvec = p->g_dtype == FA_F32 ? 4 : 8;
-    if (rows) st = check_grad("gq", p->gq, p->gq_sb, p->gq_sh, p->gq_ss, p->dk, gvec);
-    if (st == FA_OK && keys) st = check_grad("gk", p->gk, p->gk_sb, p->gk_sh, p->gk_ss, p->dk, gvec);
-    if (st == FA_OK && keys) st = check_grad("gv", p->gv, p->gv_sb, p->gv_sh, p->gv_ss, p->dv, gvec);
+    if (rows) st = check_grad("gq", p->gq, p->gq_sb, p->gq_sh, p->gq_ss, p->B, p->Hq, p->Sq, p->dk, gvec);
+    if (st == FA_OK && keys)
+        st = check_grad("gk", p->gk, p->gk_sb, p->gk_sh, p->gk_ss, p->B, p->Hkv, p->Sk, p->dk, gvec);
+    if (st == FA_OK && keys)
+        st = check_grad("gv", p->gv, p->gv_sb, p->gv_sh, p->gv_ss, p->B, p->Hkv, p->Sk, p->dv, gvec);
     if (st != FA_OK) return st;
+    // Every input is read until the last gradient is written.
+    const void *in[5] = {p->q, p->o, p->dout, p->k, p->v}, *out[3] = {p->gq, p->gk, p->gv};
+    for (int i = 0; i < 3; ++i) {
+        if (!(i ? keys : rows)) continue;
+        bool taken = false;
+        for (int j = 0; j < 5; ++j) taken |= (j < 3 ? rows : keys) && out[i] == in[j];
+        for (int j = 0; j < i; ++j) taken |= (j ? keys : rows) && out[i] == out[j];
+        if (taken) return fail(FA_ERR_INVALID_ARG, "fa_bwd: gq, gk and gv must be apart from the inputs and each other");
+    }
     if (p->mask && (((uintptr_t)p->mask & 15u) || p->m_ss % 8 || p->m_sh % 8 || p->m_sb % 8 || p->m_ss < p->Sk ||
                     p->m_sh < 0 || p->m_sb < 0))
         return fail(FA_ERR_INVALID_ARG,

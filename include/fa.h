@@ -1,6 +1,8 @@
 /*
- * fa.h -- C ABI of libfa.so: fused scaled-dot-product attention forward on
- * NVIDIA B200 (sm_100a).
+ * fa.h -- C ABI of libfa.so: fused scaled-dot-product attention on NVIDIA
+ * B200 (sm_100a): the forward pass over dense, paged and latent K and V, its
+ * gradients (fa_bwd), rotary positions (fa_rope) and the rows that a paged
+ * cache gains (fa_kv_append).
  *
  *   O = softmax(scale * Q K^T + mask) V,   LSE = log sum_j exp(scale * q.k_j)
  *
@@ -152,9 +154,11 @@ fa_status fa_fwd(const fa_fwd_params *p, void *stream);
  *   dlse: NULL, or [B, Hq, Sq] fp32 contiguous: the gradient that reaches
  *     the log-sum-exp itself.
  *   gq: [B, Hq, Sq, dk], gk: [B, Hkv, Sk, dk], gv: [B, Hkv, Sk, dv] in
- *     g_dtype, strides multiples of 8 (bf16) or 4 (fp32), each sequence
- *     stride >= the width, bases 16-byte aligned.  A KV head's gradients are
- *     the sums over its query heads.  They may not overlap the inputs.
+ *     g_dtype, strides multiples of 8 (bf16) or 4 (fp32), bases 16-byte
+ *     aligned, the three dimensions nested in any order (each stride at least
+ *     the extent of those inside it; extents of 1 take any stride).  A KV
+ *     head's gradients are the sums over its query heads.  They may overlap
+ *     neither the inputs nor one another.
  *   gsinks: NULL, or [Hq] fp32 (needs sinks): the gradient of the sinks,
  *     -sum over rows of exp(sink_h - lse) D.
  *   Rows with no visible key (lse -inf) get gq = 0 and add nothing.  There is

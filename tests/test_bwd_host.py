@@ -55,3 +55,21 @@ def test_cpu_tensors_are_refused():
     x = torch.zeros(1, 1, 2, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError):
         fa.bwd(x, x, x, x, torch.zeros(1, 1, 2), x)
+
+
+# Outputs that would overwrite themselves, each other or an input.
+@pytest.mark.parametrize("kw", [
+    dict(gk_sh=0), dict(gq_sb=0, B=2), dict(gv_ss=128, gv_sh=128), dict(gq_ss=128, gq_sh=64 * 128),
+    dict(gq=16), dict(gk=32), dict(gk=112), dict(gv=128), dict(gv=80), dict(gq=64)])
+def test_overlapping_gradients_are_refused(kw):
+    assert fa.load().fa_bwd(ctypes.byref(params(**kw)), None) == fa.FA_ERR_INVALID_ARG
+    assert b"overlap" in fa.load().fa_last_error() or b"apart" in fa.load().fa_last_error()
+
+
+# A stride that no second element uses may be anything: what stops these calls
+# is the check that comes after (the workspace).
+@pytest.mark.parametrize("kw", [
+    dict(gq_sb=3, gk_sb=0, gv_sb=-1, o_sb=5), dict(Sq=1, gq_ss=1, o_ss=1), dict(Hq=1, Hkv=1, gq_sh=0, gk_sh=7, o_sh=3),
+    dict(gq_ss=2 * 128, gq_sh=128), dict(gk_ss=3 * 256, gk_sh=128, gv_ss=3 * 256, gv_sh=128)])
+def test_layouts_of_gradients(kw):
+    assert fa.load().fa_bwd(ctypes.byref(params(workspace=0, **kw)), None) == fa.FA_ERR_WORKSPACE
