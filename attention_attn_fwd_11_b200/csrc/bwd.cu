@@ -11,7 +11,7 @@
 //   dQ_i   = scale sum_j dS_ij K_j,   dK_j = scale sum_i dS_ij Q_i
 //   dsink_h = -sum_i exp(sink_h - lse_i) D_i
 //
-// Two kernels on the caller's stream (and a third for the sinks' gradient):
+// Kernels on the caller's stream:
 //   1. bwd_prep_kernel: D and the LSE of every row, one pass over O and dO.
 //      Rows with no visible key (LSE -inf) and the padding up to a whole tile
 //      get LSE +inf, which makes every P of the row exactly 0.
@@ -21,9 +21,12 @@
 //        group: dK and dV, whose sums over the group's heads stay in the
 //        accumulators;
 //      - 128 queries of one head, walking the key tiles: dQ.
+//   3. bwd_join_kernel, where walks are so long beside the whole work that
+//      they were cut into parts for several SMs (bwd_split): adds the parts up.
+//   4. bwd_sink_kernel: the sinks' gradient, if asked for.
 // Scores and dO V^T are formed in both walks: seven matrix products where five
-// would do, but no sum crosses SMs, so nothing is accumulated with atomics in
-// HBM and the result does not depend on timing.
+// would do, but every sum has a fixed order: nothing is accumulated with
+// atomics in HBM and the result does not depend on timing.
 //
 // Both walks are one code.  An item's 128 resident rows X1, X2 (K and V; or Q
 // and dO) meet tiles of BN rows Y1, Y2 (Q and dO; or K and V):
@@ -45,6 +48,7 @@
 #include <math.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "internal.h"
 #include "score_mods.cuh"
@@ -69,6 +73,8 @@ struct BwdArgs {
     int64_t pitch;               // rows per (batch, head) of the three
     int kv_items, items;          // 128-key tiles of every KV head, then 128-query tiles of every head
     int *next;                    // first item that no CTA has taken
+    int kv_len, kv_parts, q_len, q_parts;  // walks cut into parts (see bwd_split)
+    float *kv_part, *q_part;               // and those parts' sums
     BwdGrad gq, gk, gv;
     int g_bf16;
 };
@@ -138,9 +144,10 @@ struct BwdKernel {
 };
 
 // One item: a 128-row tile x0 of (b, h) and its walk over tiles y_first ..
-// y_first + n_y - 1, for dK / dV once per head of the group.
+// y_first + n_y - 1, for dK / dV once per head of the group.  Of the whole
+// walk's tiles the item has n, from tile y of head h_first on.
 struct BwdItem {
-    int b, h, x0, y_first, n_y, n;
+    int b, h, x0, y_first, n_y, whole, n, y, h_first;
 };
 
 // Items in the order in which they are taken: dK / dV, then dQ, each with the
@@ -151,7 +158,8 @@ FA_DEV BwdItem bwd_item(const BwdArgs &a, int i) {
     BwdItem it;
     const int H = KV ? a.Hkv : a.Hq;
     const unsigned per = (unsigned)(a.B * H), idx = (unsigned)(KV ? i : i - a.kv_items);
-    const int bh = (int)(idx % per), turn = (int)(idx / per);
+    const int bh = (int)(idx % per), parts = KV ? a.kv_parts : a.q_parts, len = KV ? a.kv_len : a.q_len;
+    const int turn = (int)(idx / per) / parts, part = (int)(idx / per) % parts;
     const int xt = KV ? turn : (a.Sq + 127) / 128 - 1 - turn;
     it.b = bh / H;
     it.h = bh % H;
@@ -161,12 +169,18 @@ FA_DEV BwdItem bwd_item(const BwdArgs &a, int i) {
     if (KV) {
         if (a.causal) it.y_first = max(0, it.x0 - shift) / BN;
         it.n_y = max(0, (a.Sq + BN - 1) / BN - it.y_first);
-        it.n = it.n_y * (a.Hq / a.Hkv);
+        it.whole = it.n_y * (a.Hq / a.Hkv);
     } else {
         int last = a.Sk;  // keys visible to the tile's last row
         if (a.causal) last = min(last, min(a.Sq, it.x0 + 128) + shift);
         it.n_y = last <= 0 ? 0 : (last + BN - 1) / BN;
-        it.n = it.n_y;
+        it.whole = it.n_y;
+    }
+    it.n = it.whole, it.y = 0, it.h_first = KV ? it.h * (a.Hq / a.Hkv) : it.h;
+    if (len > 0) {
+        const int t0 = part * len;
+        it.n = min(len, max(0, it.whole - t0));
+        if (it.n > 0) it.y = t0 % it.n_y, it.h_first += t0 / it.n_y;
     }
     return it;
 }
@@ -209,7 +223,7 @@ struct BwdProducer {
         const uint32_t sb = c.sbase;
         // X of the walk before is free when its last S, its last T is done.
         const uint32_t px = ((uint32_t)walks & 1u) ^ 1u;
-        int y = 0, hy = KV ? it.h * group : it.h / group;
+        int y = it.y, hy = KV ? it.h_first : it.h / group;
         for (int t = 0; t < it.n; ++t) {
             const int y0 = (it.y_first + y) * C::BN;
             if (t == 0) {
@@ -437,7 +451,8 @@ struct BwdWorker {
         if (lane == 0) mbar_arrive(c.bar(i));
     }
 
-    FA_DEV bool item(const BwdCta &c, const BwdArgs &a, const BwdItem &it, int bars, int done, uint32_t &dones) {
+    FA_DEV bool item(const BwdCta &c, const BwdArgs &a, int index, int bars, int done, uint32_t &dones) {
+        const BwdItem it = bwd_item<KV, C::BN>(a, index);
         constexpr int BN = C::BN;
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
         const int wg = (warp >> 2) - 1;           // columns 32 wg .. 32 wg + 31 of each tile
@@ -461,7 +476,7 @@ struct BwdWorker {
         const int lim_hi = a.causal ? min(a.Sk, xr + shift + 1) : a.Sk;
         const int lim_lo = a.causal ? xr - shift : 0;
         const uint64_t sc2 = f2_pack(a.scale_log2, a.scale_log2);
-        int y = 0, hq = KV ? it.h * (a.Hq / a.Hkv) : it.h;
+        int y = it.y, hq = it.h_first;
         for (int t = 0; t < it.n; ++t) {
             const int y0 = (it.y_first + y) * BN + wg * 32;  // first column: query or key
             const float *sl = reinterpret_cast<const float *>(c.smem + C::OFF_ROW + r1.s * C::ROW_BYTES) + wg * 32;
@@ -645,6 +660,23 @@ struct BwdWorker {
         // item's products into the accumulators wait for this warp's next P
         // and dS, so they cannot come before these loads.
         const int row0 = x0 + (warp & 3) * 32, S = KV ? a.Sk : a.Sq;
+        if ((KV ? a.kv_len : a.q_len) > 0) {
+            if (it.n > 0) {
+                float4 *to = reinterpret_cast<float4 *>(KV ? a.kv_part + (int64_t)index * (128 * C::ACC)
+                                                           : a.q_part + (int64_t)(index - a.kv_items) * (128 * C::ACC)) + row;
+                for (int col = wg * 32; col < C::ACC; col += BN) {
+                    uint32_t r[32];
+                    tmem_ld32(tl + (uint32_t)(C::T_A1 + col), r);
+                    tmem_wait_ld();
+                    reg_fence(r);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        to[(col / 4 + i) * 128] = make_float4(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]),
+                                                              __uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3]));
+                }
+            }
+            return true;
+        }
         for (int col = wg * 32; col < C::ACC; col += BN) {
             const bool second = col >= DK;
             uint32_t r[32];
@@ -795,7 +827,7 @@ bwd_tile_kernel(const __grid_constant__ CUtensorMap tmQx, const __grid_constant_
         if (i >= 0 && i < a.kv_items) {
             BwdWorker<DK, DV, true, MODS, CK> w;
             while (ok && i >= 0 && i < a.kv_items) {
-                ok = w.item(c, a, bwd_item<true, BN>(a, i), K::BAR_KV, K::BAR_DONE, dones);
+                ok = w.item(c, a, i, K::BAR_KV, K::BAR_DONE, dones);
                 if (ok) i = take(++k);
             }
             // dQ's dS may lie where dK and dV were: every warp must have read them.
@@ -806,7 +838,7 @@ bwd_tile_kernel(const __grid_constant__ CUtensorMap tmQx, const __grid_constant_
         }
         BwdWorker<DK, DV, false, MODS, CQ> w;
         while (ok && i >= 0) {
-            ok = w.item(c, a, bwd_item<false, BN>(a, i), K::BAR_Q, K::BAR_DONE, dones);
+            ok = w.item(c, a, i, K::BAR_Q, K::BAR_DONE, dones);
             if (ok) i = take(++k);
         }
     }
@@ -817,6 +849,72 @@ bwd_tile_kernel(const __grid_constant__ CUtensorMap tmQx, const __grid_constant_
         tc_fence_after();
         tmem_dealloc(c.tmem, 512);
     }
+}
+
+// Sums the parts of walks that were cut: a block takes 16 columns of 128 rows,
+// first of dK and dV, then of dQ, in four groups of threads that share the
+// parts out; the order of the additions is fixed.
+template <int DK, int DV>
+__global__ void __launch_bounds__(512) bwd_join_kernel(const BwdArgs a, int kv_blocks) {
+    constexpr int BN = bwd_walk(DK);
+    __shared__ float4 others[3][4][128];
+    const int row = threadIdx.x & 127, group = threadIdx.x >> 7;
+    const auto join = [&](auto kv, int block) {
+        constexpr bool KV = decltype(kv)::value;
+        constexpr int ACC = KV ? DK + DV : DK;
+        const int tile = block / (ACC / 16), col = block % (ACC / 16) * 16;
+        const unsigned per = (unsigned)(a.B * (KV ? a.Hkv : a.Hq));
+        const int parts = KV ? a.kv_parts : a.q_parts, len = KV ? a.kv_len : a.q_len;
+        // the tile's first part; the others follow `per` items apart
+        const unsigned first = (unsigned)tile / per * (unsigned)parts * per + (unsigned)tile % per;
+        const BwdItem it = bwd_item<KV, BN>(a, (int)first + (KV ? 0 : a.kv_items));
+        const int n = (it.whole + len - 1) / len;
+        const float4 *from = reinterpret_cast<const float4 *>(KV ? a.kv_part : a.q_part) + col / 4 * 128 + row;
+        float4 s[4] = {};
+#pragma unroll 2
+        for (int p = group; p < n; p += 4) {
+            const float4 *f = from + (int64_t)(first + (unsigned)p * per) * (32 * ACC);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float4 v = __ldcg(f + i * 128);
+                s[i].x += v.x, s[i].y += v.y, s[i].z += v.z, s[i].w += v.w;
+            }
+        }
+        if (group > 0)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) others[group - 1][i][row] = s[i];
+        __syncthreads();
+        const int S = KV ? a.Sk : a.Sq;
+        if (group > 0 || it.x0 + row >= S) return;
+        const bool second = col >= DK;
+        const float f = second ? 1.f : a.scale;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int g = 0; g < 3; ++g) {
+                const float4 v = others[g][i][row];
+                s[i].x += v.x, s[i].y += v.y, s[i].z += v.z, s[i].w += v.w;
+            }
+            s[i].x *= f, s[i].y *= f, s[i].z *= f, s[i].w *= f;
+        }
+        const BwdGrad &g = KV ? (second ? a.gv : a.gk) : a.gq;
+        const int64_t at = (int64_t)it.b * g.sb + (int64_t)it.h * g.sh + (int64_t)(it.x0 + row) * g.ss + (second ? col - DK : col);
+        if (a.g_bf16) {
+            uint4 *to = reinterpret_cast<uint4 *>(g.p + 2 * at);
+#pragma unroll
+            for (int i = 0; i < 4; i += 2)
+                to[i / 2] = make_uint4(pack_bf16x2(s[i].x, s[i].y), pack_bf16x2(s[i].z, s[i].w),
+                                       pack_bf16x2(s[i + 1].x, s[i + 1].y), pack_bf16x2(s[i + 1].z, s[i + 1].w));
+        } else {
+            float4 *to = reinterpret_cast<float4 *>(g.p + 4 * at);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) to[i] = s[i];
+        }
+    };
+    if ((int)blockIdx.x < kv_blocks)
+        join(std::true_type{}, (int)blockIdx.x);
+    else
+        join(std::false_type{}, (int)blockIdx.x - kv_blocks);
 }
 
 // D and LSE of every row, DV / 8 lanes a row.  A block takes kPrepRows rows of
@@ -980,10 +1078,68 @@ cudaError_t launch_tiles(const BwdLaunch &L, const BwdArgs &a, int num_sms, cuda
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, L.tmQx, L.tmKx, L.tmVx, L.tmDOx, L.tmQy, L.tmKy, L.tmVy, L.tmDOy, a);
+    e = cudaLaunchKernelEx(&cfg, kern, L.tmQx, L.tmKx, L.tmVx, L.tmDOx, L.tmQy, L.tmKy, L.tmVy, L.tmDOy, a);
+    if (e != cudaSuccess || a.kv_len + a.q_len == 0) return e;
+    const int kv = a.kv_len ? a.kv_items / a.kv_parts * ((DK + DV) / 16) : 0;
+    const int q = a.q_len ? (a.items - a.kv_items) / a.q_parts * (DK / 16) : 0;
+    bwd_join_kernel<DK, DV><<<kv + q, 512, 0, stream>>>(a, kv);
+    return cudaGetLastError();
 }
 
 }  // namespace
+
+// Estimates in units of a tile's time (1.3 to 2 us): an item's fill, drain and
+// epilogue cost kItem tiles more, a launch of the join kernel kJoin.
+constexpr double kSms = 148, kItem = 2, kJoin = 3.5;
+
+// When the last SM is done with `nk` items of length `k` and then `nq` of
+// length `q`, each taken by whoever is free.
+double bwd_makespan(double nk, double k, double nq, double q) {
+    const double rounds = floor(nk / kSms), more = nk - rounds * kSms;  // SMs with one item more
+    const double t0 = rounds * k, t1 = t0 + k;
+    double t = (nk * k + nq * q) / kSms;
+    if (t < t0) t = t0;
+    if (more > 0 && t < t1) t = t1;
+    while (nq > 0 && more * floor(fmax(t - t1, 0) / q) + (kSms - more) * floor((t - t0) / q) < nq) t += 1;
+    return t;
+}
+
+// A walk that is longer than an SM's even share of all tiles ends last, alone:
+// few KV heads with many queries, few queries with many keys.  Such walks are
+// cut into parts of the length with the least estimate, or left whole if that
+// is less.  Measured, cut and whole: 7 heads on 1, 4000 queries, 40 keys, 128
+// wide: 28.8 and 381 us; 8 on 1, 1024 x 1024, causal: 28.7 and 117; 8 heads,
+// 16 x 4096: 24.6 and 57; 1 head, 4096 x 4096, causal: 38.6 and 63.5; but 8
+// heads, 1024 x 1024, causal (walks of 8, a share of 3.5): 28.5 and 24.5, so
+// left whole.
+BwdSplit bwd_split(int B, int Hq, int Hkv, int Sq, int Sk, int dk, int causal) {
+    BwdSplit s = {0, 1, 0, 1, 0, 0};
+    if (B <= 0 || Sq <= 0 || Sk <= 0) return s;
+    const int64_t BN = bwd_walk(dk), nk = (int64_t)B * Hkv * ((Sk + 127) / 128), nq = (int64_t)B * Hq * ((Sq + 127) / 128);
+    // The longest walks, and how long the mean one is beside it.
+    const int64_t kv = Hq / Hkv * ((Sq + BN - 1) / BN - (causal && Sq > Sk ? (Sq - Sk) / BN : 0));
+    const int64_t q = (Sk + BN - 1) / BN;
+    const double kv_mean = !causal ? 1 : Sk >= Sq ? 1 - 0.5 * Sq / Sk : 0.5;
+    const double q_mean = !causal ? 1 : Sk >= Sq ? 1 - 0.5 * Sq / Sk : 0.5 * Sk / Sq;
+    const double kv_tiles = kv_mean * (double)nk * (double)kv, q_tiles = q_mean * (double)nq * (double)q;
+    const double share = (kv_tiles + q_tiles) / kSms;
+    const int64_t longest = kv > q ? kv : q;
+    if ((double)longest <= share + kJoin) return s;
+    double best = fmax((double)longest + kItem, share + kItem * (double)(nk + nq) / kSms);
+    for (int64_t len = 2; len < longest && (double)len < 2 * share + 8; len += len < 8 ? 1 : len / 4) {
+        // parts of even length; under a causal mask the mean walk ends half a part early
+        const int64_t pk = (kv + len - 1) / len, lk = (kv + pk - 1) / pk, pq = (q + len - 1) / len, lq = (q + pq - 1) / pq;
+        const double ck = pk == 1 ? nk : ceil(causal ? kv_tiles / (double)lk + 0.5 * nk : (double)(nk * pk));
+        const double cq = pq == 1 ? nq : ceil(causal ? q_tiles / (double)lq + 0.5 * nq : (double)(nq * pq));
+        const double t = kJoin + fmax((double)(lk > lq ? lk : lq) + kItem,
+                                      bwd_makespan(ck, kv_tiles / ck + kItem, cq, q_tiles / cq + kItem));
+        if (t >= best) continue;
+        best = t;
+        s.kv_len = pk == 1 ? 0 : (int)lk, s.kv_parts = (int)pk, s.kv_chunks = pk == 1 ? 0 : nk * pk;
+        s.q_len = pq == 1 ? 0 : (int)lq, s.q_parts = (int)pq, s.q_chunks = pq == 1 ? 0 : nq * pq;
+    }
+    return s;
+}
 
 cudaError_t launch_bwd(const BwdLaunch &L, int num_sms, cudaStream_t stream) {
     const int64_t pitch = bwd_pitch(L.Sq);
@@ -1013,8 +1169,11 @@ cudaError_t launch_bwd(const BwdLaunch &L, int num_sms, cudaStream_t stream) {
     a.scale = L.scale, a.scale_log2 = L.scale * kLog2e;
     a.mods = L.mods;
     a.nlse = L.nlse, a.ndelta = L.ndelta, a.ext = static_cast<const uint4 *>(L.ext), a.pitch = pitch;
-    a.kv_items = L.B * L.Hkv * ((L.Sk + 127) / 128);
-    a.items = a.kv_items + L.B * L.Hq * ((L.Sq + 127) / 128);
+    const BwdSplit cut = bwd_split(L.B, L.Hq, L.Hkv, L.Sq, L.Sk, L.dk, L.causal);
+    a.kv_len = cut.kv_len, a.kv_parts = cut.kv_parts, a.q_len = cut.q_len, a.q_parts = cut.q_parts;
+    a.kv_part = L.part, a.q_part = L.part + cut.kv_chunks * 128 * (L.dk + L.dv);
+    a.kv_items = L.B * L.Hkv * ((L.Sk + 127) / 128) * cut.kv_parts;
+    a.items = a.kv_items + L.B * L.Hq * ((L.Sq + 127) / 128) * cut.q_parts;
     a.next = L.next;
     a.gq = BwdGrad{static_cast<char *>(L.gq), L.gq_sb, L.gq_sh, L.gq_ss};
     a.gk = BwdGrad{static_cast<char *>(L.gk), L.gk_sb, L.gk_sh, L.gk_ss};

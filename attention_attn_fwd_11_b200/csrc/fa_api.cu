@@ -404,6 +404,12 @@ size_t bwd_row_bytes(const fa_bwd_params *p) {  // of the row LSE, of D, and a q
     return (n + 255) & ~size_t(255);
 }
 
+// The rows' LSE and D, the tile counter, and the parts of walks that are cut.
+size_t bwd_bytes(const fa_bwd_params *p, bool causal) {
+    return 6 * bwd_row_bytes(p) + 256 +
+           fa::bwd_split(p->B, p->Hq, p->Hkv, p->Sq, p->Sk, p->dk, causal).bytes(p->dk, p->dv);
+}
+
 // A gradient's strides: vector stores of 16 bytes, rows that do not overlap.
 // Dimensions of extent 1 may have any stride.
 fa_status check_grad(const char *name, const void *g, int64_t sb, int64_t sh, int64_t ss, int B, int H, int S, int d,
@@ -1047,7 +1053,8 @@ fa_status fa_bwd_workspace_size(const fa_bwd_params *p, size_t *bytes) {
     fa_status st = check_bwd(p);
     if (st != FA_OK) return st;
     if (!bytes) return fail(FA_ERR_INVALID_ARG, "fa_bwd_workspace_size: bytes is NULL");
-    *bytes = 6 * bwd_row_bytes(p) + 256;
+    const size_t full = bwd_bytes(p, false), causal = bwd_bytes(p, true);
+    *bytes = full > causal ? full : causal;
     return FA_OK;
 }
 
@@ -1089,7 +1096,7 @@ fa_status fa_bwd(const fa_bwd_params *p, void *stream) {
                     p->m_sh < 0 || p->m_sb < 0))
         return fail(FA_ERR_INVALID_ARG,
                     "fa_bwd: mask must be 16-byte aligned, its strides multiples of 8 elements, m_ss >= Sk");
-    const size_t each = bwd_row_bytes(p), need = 6 * each + 256;
+    const size_t each = bwd_row_bytes(p), need = bwd_bytes(p, p->causal != 0);
     if (!p->workspace || p->workspace_bytes < need || ((uintptr_t)p->workspace & 255u))
         return fail(FA_ERR_WORKSPACE, "fa_bwd: workspace needs %zu bytes, 256-byte aligned", need);
     if (!get_encoder()) return fail(FA_ERR_CUDA, "fa_bwd: cuTensorMapEncodeTiled is not available");
@@ -1166,6 +1173,7 @@ fa_status fa_bwd(const fa_bwd_params *p, void *stream) {
     L.ndelta = reinterpret_cast<float *>(static_cast<char *>(p->workspace) + each);
     L.ext = static_cast<char *>(p->workspace) + 2 * each;
     L.next = reinterpret_cast<int *>(static_cast<char *>(p->workspace) + 6 * each);
+    L.part = reinterpret_cast<float *>(static_cast<char *>(p->workspace) + 6 * each + 256);
     int sms = 0;
     cudaError_t e = num_sms(&sms);
     if (e == cudaSuccess) e = fa::launch_bwd(L, sms, static_cast<cudaStream_t>(stream));

@@ -212,7 +212,8 @@ struct BwdLaunch {
     float *gsinks;   // NULL: not asked for
     float *nlse, *ndelta;  // workspace: [B * Hq, bwd_pitch(Sq)] each,
     void *ext;              // and as many 16-byte rows,
-    int *next;              // and the counter from which CTAs take their tiles
+    int *next;              // and the counter from which CTAs take their tiles,
+    float *part;            // and bwd_split()'s partial gradients
 };
 // Rows of nlse and ndelta per (batch, head): Sq rounded up to whole tiles,
 // walked (128 or 96) and the resident one (128) alike.
@@ -220,6 +221,17 @@ inline int64_t bwd_pitch(int Sq) { return ((int64_t)Sq + 383) / 384 * 384; }
 // Rows of a walked tile: 128, or what TMEM holds beside 192 + 128 columns of
 // dK and dV.
 constexpr int bwd_walk(int dk) { return dk == 192 ? 96 : 128; }
+// How the walks are cut into parts for different SMs: parts of at most `len`
+// tiles (0: not cut), and how many the longest walk has.  Each part's sums go
+// to the workspace and one more kernel adds them up, in order.
+struct BwdSplit {
+    int kv_len, kv_parts, q_len, q_parts;
+    int64_t kv_chunks, q_chunks;  // parts of 128 rows in the workspace
+    size_t bytes(int dk, int dv) const {
+        return 512 * ((size_t)kv_chunks * (size_t)(dk + dv) + (size_t)q_chunks * (size_t)dk);
+    }
+};
+BwdSplit bwd_split(int B, int Hq, int Hkv, int Sq, int Sk, int dk, int causal);
 cudaError_t launch_bwd(const BwdLaunch &L, int num_sms, cudaStream_t stream);
 cudaError_t bwd_device_error(int clear, int *code);
 

@@ -200,7 +200,7 @@ typedef struct {
     size_t workspace_bytes;
 } fa_bwd_params;
 
-/* Workspace bytes for these shapes; reads no pointer field. */
+/* Workspace bytes for these shapes, causal or not; reads no pointer field. */
 fa_status fa_bwd_workspace_size(const fa_bwd_params *p, size_t *bytes);
 fa_status fa_bwd(const fa_bwd_params *p, void *stream);
 

@@ -209,6 +209,49 @@ def test_many_walks_again_and_again(dk, dv):
             assert torch.equal(a, b)
 
 
+# Walks long beside the whole work, which several SMs share: few keys or KV
+# heads with many queries, few queries with many keys, parts that a causal mask
+# leaves empty, parts that end inside a head's queries.
+@pytest.mark.parametrize("Hq,Hkv,sq,sk,causal", [
+    (7, 1, 1500, 40, False), (7, 1, 1500, 40, True), (4, 1, 342, 342, True), (8, 1, 700, 130, True), (3, 3, 1, 1700, True),
+    (2, 2, 16, 2000, False), (1, 1, 1300, 1300, True), (10, 2, 777, 333, False), (9, 1, 129, 1, True), (2, 1, 1000, 1601, True)])
+@pytest.mark.parametrize("dk,dv", PAIRS)
+def test_shared_walks(Hq, Hkv, sq, sk, causal, dk, dv):
+    seed = Hq + sq + sk + dk
+    x = [torch.empty(s, dtype=torch.bfloat16, device="cuda") for s in ((2, Hq, sq, dk), (2, Hkv, sk, dk), (2, Hkv, sk, dv))]
+    rows = 6 * 4 * 2 * Hq * ((sq + 383) // 384 * 384)
+    assert fa.bwd_workspace_bytes(*x) > rows + 512  # holds parts
+    f32 = run(2, Hq, Hkv, sq, sk, dk, dv, causal, seed=seed, layout="wide", grad_dtype=torch.float32)
+    again = run(2, Hq, Hkv, sq, sk, dk, dv, causal, seed=seed, layout="wide", grad_dtype=torch.float32)
+    assert all(torch.equal(a, b) for a, b in zip(f32, again))
+    bf16 = run(2, Hq, Hkv, sq, sk, dk, dv, causal, seed=seed, layout="bshd", o_dtype=torch.bfloat16)
+    assert all(t.dtype == torch.bfloat16 for t in bf16)
+
+
+@pytest.mark.parametrize("dk,dv", PAIRS)
+@pytest.mark.parametrize("causal", [False, True])
+def test_shared_walks_with_modifiers(dk, dv, causal):
+    g = torch.Generator(device="cuda").manual_seed(dk)
+    mask = torch.randn((1, 1, 900, 208), generator=g, device="cuda").half()[..., :203]
+    mask[:, :, 40:60] = -math.inf  # rows that see nothing
+    sinks = torch.randn(6, generator=g, device="cuda")
+    run(1, 6, 1, 900, 203, dk, dv, causal, seed=dk, mask=mask, max_bias=8.0, softcap=5.0, sinks=sinks,
+        scale=1 / (5 * math.sqrt(dk)))
+
+
+def test_shared_walks_write_their_workspace_alone():
+    q, k, v, do = inputs(1, 5, 1, 1100, 70, 128, 128, seed=12)
+    o, lse = fa.fwd(q, k, v)
+    n = fa.bwd_workspace_bytes(q, k, v)
+    room = torch.full((n + 4096,), 90, dtype=torch.uint8, device="cuda")
+    want = fa.bwd(q, k, v, o, lse, do)
+    got = fa.bwd(q, k, v, o, lse, do, workspace=room[:n])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and bool((room[n:] == 90).all())
+    with pytest.raises(fa.FAError):
+        fa.bwd(q, k, v, o, lse, do, workspace=room[:n - 256])
+
+
 def test_rows_that_see_nothing_give_zeros():
     q, k, v, do = inputs(1, 2, 2, 300, 130, 128, 128, 3)
     o, lse = fa.fwd(q, k, v, causal=True)
