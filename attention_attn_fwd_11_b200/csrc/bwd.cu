@@ -93,9 +93,10 @@ struct BwdCfg {
     // step of 16 columns.
     static constexpr bool EXT = KV && !MODS;
     // Stages of Y1 and of Y2.  dQ needs the third of Y1 (K: the next tile's S
-    // comes before this tile's product with it) more than the second of Y2.
-    static constexpr int NST1 = DK == 64 ? 4 : KV ? 2 : 3;
-    static constexpr int NST2 = DK == 64 ? 4 : !KV && DK == 192 ? 1 : 2;
+    // comes before this tile's product with it) more than the second of Y2;
+    // with modifiers the room goes to the mask.
+    static constexpr int NST1 = DK == 64 ? 4 : KV || MODS ? 2 : 3;
+    static constexpr int NST2 = DK == 64 ? 4 : !KV && DK == 192 && !MODS ? 1 : 2;
     static constexpr int X_CHUNK = 128 * 128, Y_CHUNK = BN * 128;  // bytes of a 64-column chunk
     static constexpr int X1_BYTES = 128 * DK * 2, X2_BYTES = 128 * DV * 2;
     static constexpr int Y1_BYTES = BN * DK * 2, Y2_BYTES = BN * DV * 2;
@@ -134,12 +135,14 @@ struct BwdKernel {
     using CK = BwdCfg<DK, DV, true, MODS>;
     using CQ = BwdCfg<DK, DV, false, MODS>;
     static constexpr int THREADS = 128 + 32 * CK::WARPS;
-    static constexpr int OFF_BAR = CK::END > CQ::END ? CK::END : CQ::END;
+    // A warp's 32 x 32 mask values (f16), apart from both walks' tiles.
+    static constexpr int OFF_MASK = CK::END > CQ::END ? CK::END : CQ::END;
+    static constexpr int OFF_BAR = OFF_MASK + (MODS ? CK::WARPS * 2048 : 0);
     // Barriers: the item ring (full, empty), the end of a walk's products, of
     // all of them, of the last dK / dV's, the workers' change from dK / dV to
     // dQ, then both kinds' sets.
     static constexpr int BAR_DONE = 4, BAR_END = 5, BAR_KVEND = 6, BAR_MOVED = 7, BAR_KV = 8, BAR_Q = BAR_KV + CK::BARS, BARS = BAR_Q + CQ::BARS;
-    static constexpr int SMEM_BYTES = OFF_BAR + 8 * BARS + 32 + 1024;  // item ring, TMEM address, flag; alignment slack
+    static constexpr int SMEM_BYTES = OFF_BAR + 8 * BARS + 32;  // item ring, TMEM address, flag
     static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 };
 
@@ -198,7 +201,7 @@ struct Ring {
 // What every role of a CTA shares.
 struct BwdCta {
     uint8_t *smem;
-    uint32_t sbase, bar0, tmem;
+    uint32_t sbase, bar0, tmem, mask;
     volatile int *abort_flag;
     FA_DEV uint32_t bar(int i) const { return bar0 + 8u * (uint32_t)i; }
     FA_DEV bool wait(int i, uint32_t parity) const {
@@ -404,6 +407,21 @@ FA_DEV void transpose4(uint4 (&u)[4], int lane) {
     swap(u[1], u[3], 2, b1);
 }
 
+FA_DEV float lds_f16(uint32_t at) {
+    uint16_t u;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(u) : "r"(at) : "memory");
+    return __half2float(__ushort_as_half(u));
+}
+FA_DEV void lds_f16x4(uint32_t at, float (&v)[4]) {
+    __half2 h[2];
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                 : "=r"(*reinterpret_cast<uint32_t *>(&h[0])), "=r"(*reinterpret_cast<uint32_t *>(&h[1]))
+                 : "r"(at)
+                 : "memory");
+    const float2 x = __half22float2(h[0]), y = __half22float2(h[1]);
+    v[0] = x.x, v[1] = x.y, v[2] = y.x, v[3] = y.y;
+}
+
 // 32 columns (fp32 bits in r, times f) of 32 rows of a gradient: this lane's
 // row is row0 + lane, rows at or past S are not stored.
 FA_DEV void store_rows(const BwdGrad &g, int bf16, int b, int h, int row0, int S, int col, const uint32_t (&r)[32], float f,
@@ -477,51 +495,30 @@ struct BwdWorker {
         const int lim_lo = a.causal ? xr - shift : 0;
         const uint64_t sc2 = f2_pack(a.scale_log2, a.scale_log2);
         int y = it.y, hq = it.h_first;
+        // The warp's mask values of a tile, 32 queries x 32 keys, come to shared
+        // memory a tile ahead.  A query has 64 bytes, its 16-byte quarters
+        // turned so that neither eight rows' quarters nor one row's halves
+        // meet in a bank.  What lies past the end is 0: its P is 0, or its
+        // results are not stored.
+        const uint32_t ms = c.mask + (uint32_t)(warp - 4) * 2048u;
+        const auto ask_mask = [&](int head, int tile) {
+            const int walked = (it.y_first + tile) * BN + wg * 32, mine = x0 + (warp & 3) * 32;
+            const int q0 = KV ? walked : mine, key = (KV ? mine : walked) + 8 * (lane & 3);
+            const __half *m = a.mods.mask + (int64_t)it.b * a.mods.m_sb + (int64_t)head * a.mods.m_sh;
+            const int width = min(16, max(0, 2 * (a.Sk - key)));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int r = 8 * j + (lane >> 2);
+                const int bytes = q0 + r < a.Sq ? width : 0;
+                cp_async16(ms + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4), bytes ? m + (int64_t)(q0 + r) * a.mods.m_ss + key : m,
+                           bytes);
+            }
+            cp_async_commit();
+        };
+        if (MODS && masked && it.n > 0) ask_mask(hq, y);
         for (int t = 0; t < it.n; ++t) {
             const int y0 = (it.y_first + y) * BN + wg * 32;  // first column: query or key
             const float *sl = reinterpret_cast<const float *>(c.smem + C::OFF_ROW + r1.s * C::ROW_BYTES) + wg * 32;
-            // Mask values (f16 pairs) of 16 of the columns: the first half asked
-            // for before the scores are waited for, the second under the first
-            // half's work.  Rows and keys past the end read the last one's:
-            // their P is 0, or their results are not stored.
-            [[maybe_unused]] uint32_t mk[2][8];
-            const auto load_mask = [&](int half) {
-                const int f = y0 + 16 * half;
-                const uint16_t *m = reinterpret_cast<const uint16_t *>(a.mods.mask) + (int64_t)it.b * a.mods.m_sb +
-                                    (int64_t)hq * a.mods.m_sh;
-                if (KV) {
-                    m += min(xr, a.Sk - 1) + (int64_t)min(f, a.Sq - 1) * a.mods.m_ss;
-                    if (f + 16 <= a.Sq) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i, m += 2 * a.mods.m_ss)
-                            mk[half][i] = (uint32_t)__ldg(m) | (uint32_t)__ldg(m + a.mods.m_ss) << 16;
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            mk[half][i] = (uint32_t)__ldg(m);
-                            if (f + 2 * i + 1 < a.Sq) m += a.mods.m_ss;
-                            mk[half][i] |= (uint32_t)__ldg(m) << 16;
-                            if (f + 2 * i + 2 < a.Sq) m += a.mods.m_ss;
-                        }
-                    }
-                } else {
-                    m += (int64_t)min(xr, a.Sq - 1) * a.mods.m_ss;
-                    if (f + 16 <= a.Sk) {
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const uint4 w = __ldg(reinterpret_cast<const uint4 *>(m + f) + i);
-                            mk[half][4 * i] = w.x, mk[half][4 * i + 1] = w.y;
-                            mk[half][4 * i + 2] = w.z, mk[half][4 * i + 3] = w.w;
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            mk[half][i] = (uint32_t)__ldg(m + min(f + 2 * i, a.Sk - 1)) |
-                                          (uint32_t)__ldg(m + min(f + 2 * i + 1, a.Sk - 1)) << 16;
-                    }
-                }
-            };
-            if (MODS && masked) load_mask(0);
             const float slope = MODS ? alibi_slope(a.mods, hq) : 0.f;
             if (KV && MODS && !c.wait(bars + C::FULL1 + r1.s, r1.ph)) return false;
             if (!c.wait(bars + B_SFULL, tiles & 1u)) return false;
@@ -543,11 +540,14 @@ struct BwdWorker {
                 for (int j = 0; j < 4; ++j)
                     if (KV ? (y0 + i + j < lim_lo) : (y0 + i + j >= lim_hi)) v[j] = -INFINITY;
             };
+            if (MODS && masked) {
+                cp_async_wait<0>();
+                __syncwarp();
+            }
             // P (and under a softcap P ds/dz in its place in x)
             uint32_t pk[16];
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
-                if (MODS && masked && i == 0) load_mask(1);
                 float v[4] = {x[i], x[i + 1], x[i + 2], x[i + 3]};
                 float cap[4] = {1.f, 1.f, 1.f, 1.f};
                 // -LSE of the four: natural with modifiers, where the mask is
@@ -578,11 +578,17 @@ struct BwdWorker {
                         for (int j = 0; j < 4; ++j) v[j] *= a.scale_log2;
                     }
                     if (masked) {
+                        float m[4];
+                        if (KV) {
 #pragma unroll
-                        for (int j = 0; j < 4; j += 2) {
-                            const float2 m = __half22float2(*reinterpret_cast<const __half2 *>(&mk[i / 16][(i + j) % 16 / 2]));
-                            nl[j / 2] = f2_fma(f2_pack(m.x, m.y), f2_pack(slope, slope), nl[j / 2]);
+                            for (int j = 0; j < 4; ++j)
+                                m[j] = lds_f16(ms + (i + j) * 64 + (((lane >> 3) ^ ((i + j) >> 1 & 3)) << 4) + 2 * (lane & 7));
+                        } else {
+                            lds_f16x4(ms + lane * 64 + (((i >> 3) ^ (lane >> 1 & 3)) << 4) + (i & 4) * 2, m);
                         }
+#pragma unroll
+                        for (int j = 0; j < 4; j += 2)
+                            nl[j / 2] = f2_fma(f2_pack(m[j], m[j + 1]), f2_pack(slope, slope), nl[j / 2]);
                     }
                 }
                 if (edge) hide(v, i);
@@ -598,6 +604,13 @@ struct BwdWorker {
                     x[k + 1] = ex2(e1);
                     pk[k / 2] = pack_bf16x2(x[k], x[k + 1]);
                     if (capped) f2_unpack(f2_mul(f2_pack(x[k], x[k + 1]), f2_pack(cap[2 * j], cap[2 * j + 1])), x[k], x[k + 1]);
+                }
+            }
+            if (MODS && masked) {
+                __syncwarp();
+                if (t + 1 < it.n) {
+                    const bool wrap = y + 1 == it.n_y;
+                    ask_mask(wrap ? hq + 1 : hq, wrap ? 0 : y + 1);
                 }
             }
             if (KV) {
@@ -706,10 +719,11 @@ bwd_tile_kernel(const __grid_constant__ CUtensorMap tmQx, const __grid_constant_
     using CK = typename K::CK;
     using CQ = typename K::CQ;
     constexpr int BN = CK::BN, WARPS = CK::WARPS;
-    extern __shared__ uint8_t smem_raw[];
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
     BwdCta c;
-    c.smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    c.smem = smem_raw;
     c.sbase = smem_u32(c.smem);
+    c.mask = c.sbase + K::OFF_MASK;
     uint64_t *bars = reinterpret_cast<uint64_t *>(c.smem + K::OFF_BAR);
     c.bar0 = smem_u32(bars);
     volatile int *slot = reinterpret_cast<volatile int *>(bars + K::BARS);  // two items
@@ -841,6 +855,7 @@ bwd_tile_kernel(const __grid_constant__ CUtensorMap tmQx, const __grid_constant_
             ok = w.item(c, a, i, K::BAR_Q, K::BAR_DONE, dones);
             if (ok) i = take(++k);
         }
+        if (MODS) cp_async_wait<0>();  // (after an abort)
     }
 
     tc_fence_before();

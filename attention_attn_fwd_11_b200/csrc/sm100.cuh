@@ -237,6 +237,12 @@ FA_DEV void cp_async16(uint32_t dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src))
                  : "memory");
 }
+// The first `bytes` (0 to 16) of the source, zeros after them.
+FA_DEV void cp_async16(uint32_t dst, const void *src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)),
+                 "r"(bytes)
+                 : "memory");
+}
 FA_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // The mbarrier receives one arrival (counted against its expected count)
 // once every cp.async this thread issued so far has completed.
