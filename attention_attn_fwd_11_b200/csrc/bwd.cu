@@ -23,7 +23,6 @@
 //      - 128 queries of one head, walking the key tiles: dQ.
 //   3. bwd_join_kernel, where walks are so long beside the whole work that
 //      they were cut into parts for several SMs (bwd_split): adds the parts up.
-//   4. bwd_sink_kernel: the sinks' gradient, if asked for.
 // Scores and dO V^T are formed in both walks: seven matrix products where five
 // would do, but every sum has a fixed order: nothing is accumulated with
 // atomics in HBM and the result does not depend on timing.
@@ -38,6 +37,7 @@
 //   warp 0      TMA producer: X1, X2 once, then rings of Y1 (with the LSE and
 //               D of its rows) and Y2 tiles.
 //   warp 1      MMA issuer (whole warp, one elected lane issues).
+//   warp 2      the sinks' gradient, if asked for.
 //   warps 4 ..  BN / 32 warpgroups, each 32 of the tile's columns: P from S,
 //               then dS from P and T, both as bf16 A operands in TMEM, so that
 //               those products read only Y from shared memory.
@@ -77,6 +77,7 @@ struct BwdArgs {
     float *kv_part, *q_part;               // and those parts' sums
     BwdGrad gq, gk, gv;
     int g_bf16;
+    float *gsinks;  // NULL: not asked for
 };
 
 // (dS is ready on two barriers in turn: dQ's workers may finish a tile before
@@ -708,6 +709,23 @@ struct BwdWorker {
     }
 };
 
+// ---- warp 2: the sinks' gradient, a head at a time ---------------------------
+// A double a lane, in the order of the rows, and then the lanes.
+FA_DEV void sink_gradients(const BwdArgs &a, int lane) {
+    for (int h = blockIdx.x; h < a.Hq; h += gridDim.x) {
+        const float sk = __ldg(a.mods.sinks + h);
+        double s = 0;
+        for (int b = 0; b < a.B; ++b) {
+            const int64_t r = ((int64_t)b * a.Hq + h) * a.pitch;
+#pragma unroll 4
+            for (int i = lane; i < a.Sq; i += 32) s += ex2((sk + __ldg(a.nlse + r + i)) * kLog2e) * __ldg(a.ndelta + r + i);
+        }
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+        if (lane == 0) a.gsinks[h] = (float)s;
+    }
+}
+
 // Persistent: one CTA an SM takes items from a counter until none is left.
 template <int DK, int DV, bool MODS>
 __global__ void __launch_bounds__(BwdKernel<DK, DV, MODS>::THREADS, 1)
@@ -833,6 +851,8 @@ bwd_tile_kernel(const __grid_constant__ CUtensorMap tmQx, const __grid_constant_
         mma_commit_warp(c.bar(K::BAR_END));
         mbar_wait_drain(c.bar(K::BAR_END), 0);
         __syncwarp();
+    } else if (warp == 2) {
+        if (a.gsinks) sink_gradients(a, lane);
     } else if (warp >= 4) {
         // All of dK / dV, then all of dQ (the list's order).
         uint32_t dones = 0;
@@ -1043,28 +1063,6 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const PrepArgs a) {
     }
 }
 
-// dsink_h: one block a head, rows in a fixed order.
-__global__ void __launch_bounds__(512) bwd_sink_kernel(const float *nlse, const float *ndelta, int64_t pitch, int B,
-                                                       int Hq, int Sq, const float *sinks, float *out) {
-    __shared__ float part[16];
-    const int h = blockIdx.x;
-    const float sk = sinks[h];
-    float acc = 0.f;
-    for (int b = 0; b < B; ++b) {
-        const int64_t r = ((int64_t)b * Hq + h) * pitch;
-        for (int i = threadIdx.x; i < Sq; i += 512) acc += ex2((sk + nlse[r + i]) * kLog2e) * ndelta[r + i];
-    }
-#pragma unroll
-    for (int k = 16; k > 0; k >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, k);
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = acc;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        float s = 0.f;
-        for (int w = 0; w < 16; ++w) s += part[w];
-        out[h] = s;
-    }
-}
-
 template <int DK, int DV, bool MODS>
 cudaError_t launch_tiles(const BwdLaunch &L, const BwdArgs &a, int num_sms, cudaStream_t stream) {
     using K = BwdKernel<DK, DV, MODS>;
@@ -1080,7 +1078,8 @@ cudaError_t launch_tiles(const BwdLaunch &L, const BwdArgs &a, int num_sms, cuda
         if (e != cudaSuccess) return e;
         set.fetch_or(bit, std::memory_order_relaxed);
     }
-    const int grid = a.items < num_sms ? a.items : num_sms;
+    int grid = a.items < num_sms ? a.items : num_sms;
+    if (grid == 0 && a.gsinks) grid = 1;
     if (grid == 0) return cudaSuccess;
     // Starts under the row kernel's end and waits for it on the device.
     cudaLaunchConfig_t cfg = {};
@@ -1194,6 +1193,7 @@ cudaError_t launch_bwd(const BwdLaunch &L, int num_sms, cudaStream_t stream) {
     a.gk = BwdGrad{static_cast<char *>(L.gk), L.gk_sb, L.gk_sh, L.gk_ss};
     a.gv = BwdGrad{static_cast<char *>(L.gv), L.gv_sb, L.gv_sh, L.gv_ss};
     a.g_bf16 = L.g_bf16;
+    a.gsinks = L.gsinks;
 #define FA_BWD_PAIR(DK_, DV_) \
     (L.has_mods ? launch_tiles<DK_, DV_, true>(L, a, num_sms, stream) : launch_tiles<DK_, DV_, false>(L, a, num_sms, stream))
     cudaError_t e = cudaErrorInvalidValue;
@@ -1201,10 +1201,6 @@ cudaError_t launch_bwd(const BwdLaunch &L, int num_sms, cudaStream_t stream) {
     if (L.dk == 128 && L.dv == 128) e = FA_BWD_PAIR(128, 128);
     if (L.dk == 192 && L.dv == 128) e = FA_BWD_PAIR(192, 128);
 #undef FA_BWD_PAIR
-    if (e == cudaSuccess && L.gsinks) {
-        bwd_sink_kernel<<<L.Hq, 512, 0, stream>>>(L.nlse, L.ndelta, pitch, L.B, L.Hq, L.Sq, L.mods.sinks, L.gsinks);
-        e = cudaGetLastError();
-    }
     return e;
 }
 
