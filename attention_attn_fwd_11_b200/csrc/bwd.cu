@@ -163,7 +163,8 @@ FA_DEV BwdItem bwd_item(const BwdArgs &a, int i) {
     const int H = KV ? a.Hkv : a.Hq;
     const unsigned per = (unsigned)(a.B * H), idx = (unsigned)(KV ? i : i - a.kv_items);
     const int bh = (int)(idx % per), parts = KV ? a.kv_parts : a.q_parts, len = KV ? a.kv_len : a.q_len;
-    const int turn = (int)(idx / per) / parts, part = (int)(idx / per) % parts;
+    int turn = (int)(idx / per), part = 0;
+    if (len > 0) part = turn % parts, turn /= parts;
     const int xt = KV ? turn : (a.Sq + 127) / 128 - 1 - turn;
     it.b = bh / H;
     it.h = bh % H;
@@ -1145,6 +1146,7 @@ BwdSplit bwd_split(int B, int Hq, int Hkv, int Sq, int Sk, int dk, int causal) {
         const int64_t pk = (kv + len - 1) / len, lk = (kv + pk - 1) / pk, pq = (q + len - 1) / len, lq = (q + pq - 1) / pq;
         const double ck = pk == 1 ? nk : ceil(causal ? kv_tiles / (double)lk + 0.5 * nk : (double)(nk * pk));
         const double cq = pq == 1 ? nq : ceil(causal ? q_tiles / (double)lq + 0.5 * nq : (double)(nq * pq));
+        if (kJoin + share + kItem * (ck + cq) / kSms >= best) continue;  // the even share alone
         const double t = kJoin + fmax((double)(lk > lq ? lk : lq) + kItem,
                                       bwd_makespan(ck, kv_tiles / ck + kItem, cq, q_tiles / cq + kItem));
         if (t >= best) continue;
