@@ -178,6 +178,15 @@ def _stream(stream):
     return _vp(stream.cuda_stream)
 
 
+def _used_on(stream, *made):
+    """For tensors made here, on the current stream, whose kernels run on a
+    given one: their memory is not to be handed out before those are done."""
+    if stream is not None:
+        for t in made:
+            if t is not None:
+                t.record_stream(stream)
+
+
 def _need_cuda(*ts):
     for t in ts:
         if t is not None and not t.is_cuda:
@@ -352,6 +361,7 @@ def bwd(q, k, v, o, lse, do, scale=None, causal=False, mask=None, max_bias=0.0, 
         workspace = torch.empty(n.value, device=q.device, dtype=torch.uint8)
     p.workspace, p.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _check(lib.fa_bwd(ref, _stream(stream)))
+    _used_on(stream, workspace, dq, dk, dv, dsinks)
     return (dq, dk, dv) if sinks is None else (dq, dk, dv, dsinks)
 
 
@@ -790,6 +800,7 @@ def rope(q, inv_freq, k=None, pos=None, pos0=0, interleaved=False, offset=0, inv
     p.inv_freq, p.rot_dim, p.rot_offset = inv_freq.data_ptr(), 2 * inv_freq.numel(), offset
     p.interleaved, p.inverse, p.mscale = int(interleaved), int(inverse), mscale
     _check(load().fa_rope(ctypes.byref(p), _stream(stream)))
+    _used_on(stream, out, k_out)
     return out, k_out
 
 
@@ -859,4 +870,5 @@ def kv_append(k, v, k_cache, v_cache, block_table, seq_lens, q_lens=None, inv_fr
     elif q_out is not None:
         raise ValueError("q_out without q")
     _check(load().fa_kv_append(ctypes.byref(p), _stream(stream)))
+    _used_on(stream, q_out)
     return q_out

@@ -398,6 +398,38 @@ def test_captured_and_replayed_on_another_stream():
         assert torch.equal(a, b)
 
 
+def test_on_a_given_stream_that_is_still_busy():
+    """The workspace made inside outlives the call until its kernels are done."""
+    q, k, v, do = inputs(1, 5, 1, 1100, 70, 128, 128, seed=3)
+    o, lse = fa.fwd(q, k, v)
+    want = fa.bwd(q, k, v, o, lse, do)
+    n = fa.bwd_workspace_bytes(q, k, v)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)  # some 10 ms
+    got = fa.bwd(q, k, v, o, lse, do, stream=side)
+    others = [torch.full((n,), 90, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and all(bool((t == 90).all()) for t in others)
+
+
+def test_two_calls_at_once():
+    cases = [inputs(1, 7, 1, 1500, 40, 128, 128, seed=1), inputs(2, 8, 8, 700, 700, 64, 64, seed=2)]
+    fwd = [fa.fwd(*c[:3], causal=True) for c in cases]
+    want = [fa.bwd(*c[:3], o, lse, c[3], causal=True) for c, (o, lse) in zip(cases, fwd)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(5):
+        for i, (c, (o, lse)) in enumerate(zip(cases, fwd)):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(fa.bwd(*c[:3], o, lse, c[3], causal=True))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(a, b) for r in got[i] for a, b in zip(r, want[i]))
+
+
 def test_refusals():
     q, k, v, do = inputs(1, 4, 2, 20, 30, 64, 64, 61)
     o, lse = fa.fwd(q, k, v)
