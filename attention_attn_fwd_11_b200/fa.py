@@ -9,6 +9,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 
 import torch
 
@@ -105,6 +106,25 @@ class KvAppendParams(ctypes.Structure):
                 ("pos", _vp), ("pos_sb", _i64), ("q", _vp), ("q_out", _vp), ("Hq", _i32), ("q_sb", _i64),
                 ("q_sh", _i64), ("q_ss", _i64), ("qo_sb", _i64), ("qo_sh", _i64), ("qo_ss", _i64)]
 
+
+def _packer(cls, n):
+    """A function that makes a cls from its first n fields; the others are 0.
+    (One struct.pack: ctypes sets fields one by one, 6 us for 45 of them
+    where this takes 1.5.)"""
+    codes = {_vp: "P", _i32: "i", _i64: "q", ctypes.c_float: "f", ctypes.c_size_t: "N"}
+    fields = "@" + "".join(codes[t] for _, t in cls._fields_[:n])
+    whole = struct.Struct("%s%dx" % (fields, ctypes.sizeof(cls) - struct.calcsize(fields)))
+
+    def make(*values):
+        try:
+            return cls.from_buffer_copy(whole.pack(*values))
+        except struct.error as e:
+            raise ValueError("an argument is out of its type's range: %s" % e) from None
+
+    return make
+
+
+_pack_bwd, _pack_rope, _pack_append = _packer(BwdParams, 45), _packer(RopeParams, 31), _packer(KvAppendParams, 22)
 
 FA_KV_Q8_0, FA_KV_Q4_0, FA_KV_FP8_E4M3 = 8, 4, 2
 KV_QUANT = {"q8_0": (FA_KV_Q8_0, 34), "q4_0": (FA_KV_Q4_0, 18),
@@ -334,10 +354,11 @@ def bwd(q, k, v, o, lse, do, scale=None, causal=False, mask=None, max_bias=0.0, 
     c0, c1, c2, c3 = dv.stride()
     if not q3 == k3 == v3 == o3 == g3 == a3 == b3 == c3 == 1:
         raise ValueError("the last dim of q, k, v, o, do and the gradients must be contiguous")
-    p = BwdParams(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(), lse.data_ptr(), _ptr(dlse),
-                  dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, Hq, Hkv, Sq, Sk, hd, vd, q0, q1, q2, k0, k1, k2,
-                  v0, v1, v2, o0, o1, o2, g0, g1, g2, a0, a1, a2, b0, b1, b2, c0, c1, c2,
-                  1.0 / math.sqrt(hd) if scale is None else scale, 1 if causal else 0, _odt(o.dtype), _odt(dq.dtype))
+    p = _pack_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(), lse.data_ptr(),
+                  dlse.data_ptr() if dlse is not None else 0, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                  B, Hq, Hkv, Sq, Sk, hd, vd, q0, q1, q2, k0, k1, k2, v0, v1, v2, o0, o1, o2, g0, g1, g2, a0, a1, a2,
+                  b0, b1, b2, c0, c1, c2, 1.0 / math.sqrt(hd) if scale is None else scale, 1 if causal else 0,
+                  _odt(o.dtype), _odt(dq.dtype))
     if mask is not None:  # [Bm, Hm, Sq, Sk] f16; a size-1 batch or head dim broadcasts
         if (mask.dtype != torch.float16 or mask.dim() != 4 or mask.stride(3) != 1 or mask.shape[0] not in (1, B) or
                 mask.shape[1] not in (1, Hq) or mask.shape[2:] != (Sq, Sk)):
@@ -778,27 +799,24 @@ def rope(q, inv_freq, k=None, pos=None, pos0=0, interleaved=False, offset=0, inv
     o0, o1, o2, o3 = out.stride()
     if out.shape != qs or out.dtype != dtype or q3 != 1 or o3 != 1:
         raise ValueError("an output must have its input's shape and dtype, and all a contiguous last dim")
-    p = RopeParams(q.data_ptr(), out.data_ptr(), q0, q1, q2, o0, o1, o2)
+    k_in, k_made, Hk, k0, k1, k2, k3, r0, r1, r2, r3 = 0, 0, 0, 0, 0, 0, 1, 0, 0, 0, 1
     if k is not None:
         ks = k.shape
         if k.dtype != dtype or len(ks) != 4 or ks[0] != B or ks[2] != S or ks[3] != d:
             raise ValueError("k must be [B, Hk, S, d] with q's dtype, B, S and d")
         if k_out is None:
             k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
-        q0, q1, q2, q3 = k.stride()
-        o0, o1, o2, o3 = k_out.stride()
-        if k_out.shape != ks or k_out.dtype != dtype or q3 != 1 or o3 != 1:
+        k0, k1, k2, k3 = k.stride()
+        r0, r1, r2, r3 = k_out.stride()
+        if k_out.shape != ks or k_out.dtype != dtype or k3 != 1 or r3 != 1:
             raise ValueError("an output must have its input's shape and dtype, and all a contiguous last dim")
-        p.k, p.k_out, p.Hk = k.data_ptr(), k_out.data_ptr(), ks[1]
-        p.k_sb, p.k_sh, p.k_ss, p.ko_sb, p.ko_sh, p.ko_ss = q0, q1, q2, o0, o1, o2
+        k_in, k_made, Hk = k.data_ptr(), k_out.data_ptr(), ks[1]
     elif k_out is not None:
         raise ValueError("k_out without k")
-    p.B, p.Hq, p.S, p.d, p.dtype = B, Hq, S, d, _odt(dtype)
-    if pos is not None:
-        p.pos_sb, p.pos = _check_pos(pos, B, S), pos.data_ptr()
-    p.pos0 = pos0
-    p.inv_freq, p.rot_dim, p.rot_offset = inv_freq.data_ptr(), 2 * inv_freq.numel(), offset
-    p.interleaved, p.inverse, p.mscale = int(interleaved), int(inverse), mscale
+    pos_sb, pos_in = (0, 0) if pos is None else (_check_pos(pos, B, S), pos.data_ptr())
+    p = _pack_rope(q.data_ptr(), out.data_ptr(), q0, q1, q2, o0, o1, o2, k_in, k_made, k0, k1, k2, r0, r1, r2, B, Hq, Hk,
+                   S, d, _odt(dtype), pos_in, pos_sb, pos0, inv_freq.data_ptr(), 2 * inv_freq.numel(), offset,
+                   1 if interleaved else 0, 1 if inverse else 0, mscale)
     _check(load().fa_rope(ctypes.byref(p), _stream(stream)))
     _used_on(stream, out, k_out)
     return out, k_out
@@ -835,9 +853,9 @@ def kv_append(k, v, k_cache, v_cache, block_table, seq_lens, q_lens=None, inv_fr
     for t, dim in ((block_table, 2), (seq_lens, 1), (q_lens, 1)):
         if t is not None and (t.dtype != torch.int32 or t.dim() != dim or t.shape[0] != B or not t.is_contiguous()):
             raise ValueError("block_table [B, max_blocks], seq_lens [B] and q_lens [B] must be contiguous int32")
-    p = KvAppendParams(k.data_ptr(), v.data_ptr(), k0, k1, k2, v0, v1, v2, k_cache.data_ptr(), v_cache.data_ptr(),
-                       block_table.data_ptr(), seq_lens.data_ptr(), _ptr(q_lens), block_table.shape[1], B, Hkv, Sq, dk,
-                       dv, cs[2], cs[0])
+    p = _pack_append(k.data_ptr(), v.data_ptr(), k0, k1, k2, v0, v1, v2, k_cache.data_ptr(), v_cache.data_ptr(),
+                     block_table.data_ptr(), seq_lens.data_ptr(), q_lens.data_ptr() if q_lens is not None else 0,
+                     block_table.shape[1], B, Hkv, Sq, dk, dv, cs[2], cs[0], 0)
     if ctype != bf16:
         kv_type, _ = _paged_kv(k, k_cache, kv_type)
         code, per = KV_QUANT[kv_type]

@@ -113,3 +113,19 @@ def test_cpu_tensors_are_refused():
         fa.rope(x, inv)
     with pytest.raises(ValueError):
         fa.kv_append(x, x, x, x, torch.zeros(1, 1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("cls,pack,n", [(fa.BwdParams, fa._pack_bwd, 45), (fa.RopeParams, fa._pack_rope, 31),
+                                        (fa.KvAppendParams, fa._pack_append, 22)])
+def test_packed_arguments(cls, pack, n):
+    """Every field gets its value, the rest 0; what a field cannot hold is refused."""
+    p = pack(*range(1, n + 1))
+    for i, (name, _) in enumerate(cls._fields_):
+        assert (getattr(p, name) or 0) == (i + 1 if i < n else 0), name
+    ints = [i for i, (_, t) in enumerate(cls._fields_[:n]) if t is ctypes.c_int]
+    for bad in (1 << 31, -(1 << 31) - 1):
+        with pytest.raises(ValueError):
+            pack(*[bad if i == ints[0] else 1 for i in range(n)])
+    for i, (name, t) in enumerate(cls._fields_[:n]):
+        if t is ctypes.c_float:  # as in C; the library refuses it
+            assert getattr(pack(*[1e300 if j == i else 1 for j in range(n)]), name) == math.inf
