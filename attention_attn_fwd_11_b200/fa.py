@@ -627,14 +627,17 @@ def _dequant_entry(src, qtype, row_elems, out, kv_scale=1.0):
         raise ValueError("src must be uint8 blocks")
     if src.stride(-1) != 1:
         raise ValueError("src rows must be contiguous")
-    lead = src.shape[:-1]
+    *lead, width = src.shape
+    whole = src.is_contiguous()
     if out is None:
-        out = src.new_empty(lead + (row_elems,), dtype=torch.bfloat16)
-    if out.dtype != torch.bfloat16 or out.shape[:-1] != lead or out.shape[-1] < row_elems or out.stride(-1) != 1:
-        raise ValueError("out must be bf16 [..., >= row_elems] with the rows of src")
-    if src.is_contiguous() and out.is_contiguous() and src.dim() > 1 and src.shape[-1] > 0:
+        out = torch.empty((*lead, row_elems), device=src.device, dtype=torch.bfloat16)
+    else:
+        shape = out.shape
+        if out.dtype != torch.bfloat16 or [*shape[:-1]] != lead or shape[-1] < row_elems or out.stride(-1) != 1:
+            raise ValueError("out must be bf16 [..., >= row_elems] with the rows of src")
+        whole = whole and out.is_contiguous()
+    if whole and lead and width > 0:
         # one row stride each, without building the 2-D views (6 us of host time for two tensors)
-        width = src.shape[-1]
         return KvDequantParams(src.data_ptr(), KV_QUANT[qtype][0], src.numel() // width, row_elems, width,
                                out.data_ptr(), out.shape[-1], kv_scale), out
     s2, o2 = src.reshape(-1, src.shape[-1]), out.reshape(-1, out.shape[-1])
