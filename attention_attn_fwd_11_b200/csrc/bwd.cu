@@ -420,21 +420,6 @@ FA_DEV void transpose4(uint4 (&u)[4], int lane) {
     swap(u[1], u[3], 2, b1);
 }
 
-FA_DEV float lds_f16(uint32_t at) {
-    uint16_t u;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(u) : "r"(at) : "memory");
-    return __half2float(__ushort_as_half(u));
-}
-FA_DEV void lds_f16x4(uint32_t at, float (&v)[4]) {
-    __half2 h[2];
-    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
-                 : "=r"(*reinterpret_cast<uint32_t *>(&h[0])), "=r"(*reinterpret_cast<uint32_t *>(&h[1]))
-                 : "r"(at)
-                 : "memory");
-    const float2 x = __half22float2(h[0]), y = __half22float2(h[1]);
-    v[0] = x.x, v[1] = x.y, v[2] = y.x, v[3] = y.y;
-}
-
 // 32 columns (fp32 bits in r, times f) of 32 rows of a gradient: this lane's
 // row is row0 + lane, rows at or past S are not stored.
 FA_DEV void store_rows(const BwdGrad &g, int bf16, int b, int h, int row0, int S, int col, const uint32_t (&r)[32], float f,
@@ -513,7 +498,8 @@ struct BwdWorker {
         // turned so that neither eight rows' quarters nor one row's halves
         // meet in a bank.  What lies past the end is 0: its P is 0, or its
         // results are not stored.
-        const uint32_t ms = c.mask + (uint32_t)(warp - 4) * 2048u;
+        const uint8_t *mv = c.smem + c.mask + (warp - 4) * 2048;
+        const uint32_t ms = smem_u32(mv);
         const auto ask_mask = [&](int head, int tile) {
             const int walked = (it.y_first + tile) * BN + wg * 32, mine = x0 + (warp & 3) * 32;
             const int q0 = KV ? walked : mine, key = (KV ? mine : walked) + 8 * (lane & 3);
@@ -559,66 +545,82 @@ struct BwdWorker {
             }
             // P (and under a softcap P ds/dz in its place in x)
             uint32_t pk[16];
+            // (One form for each set of modifiers: branches inside would keep
+            // the columns' chains from overlapping.)
+            const auto probabilities = [&](auto capped_, auto masked_) {
+                constexpr bool CAPPED = decltype(capped_)::value, MASKED = decltype(masked_)::value;
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-                float v[4] = {x[i], x[i + 1], x[i + 2], x[i + 3]};
-                float cap[4] = {1.f, 1.f, 1.f, 1.f};
-                // -LSE of the four: natural with modifiers, where the mask is
-                // added to it first (both may be as large as the mask's lowest
-                // value, and their sum is what counts), else in base 2
-                uint64_t nl[2];
-                if (C::EXT) {
-                    nl[0] = nl[1] = 0;
-                } else if (KV) {
-                    const ulonglong2 l = *reinterpret_cast<const ulonglong2 *>(sl + i);
-                    nl[0] = l.x, nl[1] = l.y;
-                } else {
-                    nl[0] = nl[1] = f2_pack(row_nlse, row_nlse);
-                }
-                if constexpr (MODS) {
-                    if (capped) {
-                        // softcap (1 - tanh^2), as softcap - (v root)^2
-                        softcap4(v, a.scale, a.mods.softcap);
-#pragma unroll
-                        for (int j = 0; j < 4; j += 2) {
-                            const uint64_t w = f2_pack(v[j], v[j + 1]);
-                            f2_unpack(f2_fma(f2_mul(w, f2_pack(-root, -root)), f2_mul(w, f2_pack(root, root)),
-                                             f2_pack(a.mods.softcap, a.mods.softcap)),
-                                      cap[j], cap[j + 1]);
-                        }
+                for (int i = 0; i < 32; i += 4) {
+                    float v[4] = {x[i], x[i + 1], x[i + 2], x[i + 3]};
+                    float cap[4] = {1.f, 1.f, 1.f, 1.f};
+                    // -LSE of the four: natural with modifiers, where the mask is
+                    // added to it first (both may be as large as the mask's lowest
+                    // value, and their sum is what counts), else in base 2
+                    uint64_t nl[2];
+                    if (C::EXT) {
+                        nl[0] = nl[1] = 0;
+                    } else if (KV) {
+                        const ulonglong2 l = *reinterpret_cast<const ulonglong2 *>(sl + i);
+                        nl[0] = l.x, nl[1] = l.y;
                     } else {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) v[j] *= a.scale_log2;
+                        nl[0] = nl[1] = f2_pack(row_nlse, row_nlse);
                     }
-                    if (masked) {
-                        float m[4];
-                        if (KV) {
+                    if constexpr (MODS) {
+                        if constexpr (CAPPED) {
+                            // softcap (1 - tanh^2), as softcap - (v root)^2
+                            softcap4(v, a.scale, a.mods.softcap);
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                m[j] = lds_f16(ms + (i + j) * 64 + (((lane >> 3) ^ ((i + j) >> 1 & 3)) << 4) + 2 * (lane & 7));
+                            for (int j = 0; j < 4; j += 2) {
+                                const uint64_t w = f2_pack(v[j], v[j + 1]);
+                                f2_unpack(f2_fma(f2_mul(w, f2_pack(-root, -root)), f2_mul(w, f2_pack(root, root)),
+                                                 f2_pack(a.mods.softcap, a.mods.softcap)),
+                                          cap[j], cap[j + 1]);
+                            }
                         } else {
-                            lds_f16x4(ms + lane * 64 + (((i >> 3) ^ (lane >> 1 & 3)) << 4) + (i & 4) * 2, m);
-                        }
 #pragma unroll
-                        for (int j = 0; j < 4; j += 2)
-                            nl[j / 2] = f2_fma(f2_pack(m[j], m[j + 1]), f2_pack(slope, slope), nl[j / 2]);
+                            for (int j = 0; j < 4; ++j) v[j] *= a.scale_log2;
+                        }
+                        if constexpr (MASKED) {
+                            float m[4];
+                            if (KV) {
+#pragma unroll
+                                for (int j = 0; j < 4; ++j)
+                                    m[j] = __half2float(*reinterpret_cast<const __half *>(
+                                        mv + (i + j) * 64 + (((lane >> 3) ^ ((i + j) >> 1 & 3)) << 4) + 2 * (lane & 7)));
+                            } else {
+                                const uint2 w = *reinterpret_cast<const uint2 *>(
+                                    mv + lane * 64 + (((i >> 3) ^ (lane >> 1 & 3)) << 4) + (i & 4) * 2);
+                                const float2 lo = __half22float2(*reinterpret_cast<const __half2 *>(&w.x));
+                                const float2 hi = __half22float2(*reinterpret_cast<const __half2 *>(&w.y));
+                                m[0] = lo.x, m[1] = lo.y, m[2] = hi.x, m[3] = hi.y;
+                            }
+#pragma unroll
+                            for (int j = 0; j < 4; j += 2)
+                                nl[j / 2] = f2_fma(f2_pack(m[j], m[j + 1]), f2_pack(slope, slope), nl[j / 2]);
+                        }
+                    }
+                    if (edge) hide(v, i);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int k = i + 2 * j;
+                        const uint64_t xx = f2_pack(v[2 * j], v[2 * j + 1]);
+                        float e0, e1;
+                        f2_unpack(C::EXT ? f2_mul(xx, sc2)
+                                  : MODS ? f2_fma(nl[j], f2_pack(kLog2e, kLog2e), xx)
+                                         : f2_fma(xx, sc2, nl[j]), e0, e1);
+                        x[k] = ex2(e0);
+                        x[k + 1] = ex2(e1);
+                        pk[k / 2] = pack_bf16x2(x[k], x[k + 1]);
+                        if constexpr (CAPPED) f2_unpack(f2_mul(f2_pack(x[k], x[k + 1]), f2_pack(cap[2 * j], cap[2 * j + 1])), x[k], x[k + 1]);
                     }
                 }
-                if (edge) hide(v, i);
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int k = i + 2 * j;
-                    const uint64_t xx = f2_pack(v[2 * j], v[2 * j + 1]);
-                    float e0, e1;
-                    f2_unpack(C::EXT ? f2_mul(xx, sc2)
-                              : MODS ? f2_fma(nl[j], f2_pack(kLog2e, kLog2e), xx)
-                                     : f2_fma(xx, sc2, nl[j]), e0, e1);
-                    x[k] = ex2(e0);
-                    x[k + 1] = ex2(e1);
-                    pk[k / 2] = pack_bf16x2(x[k], x[k + 1]);
-                    if (capped) f2_unpack(f2_mul(f2_pack(x[k], x[k + 1]), f2_pack(cap[2 * j], cap[2 * j + 1])), x[k], x[k + 1]);
-                }
-            }
+            };
+            constexpr std::true_type yes;
+            constexpr std::false_type no;
+            if (capped)
+                masked ? probabilities(yes, yes) : probabilities(yes, no);
+            else
+                masked ? probabilities(no, yes) : probabilities(no, no);
             if (MODS && masked) {
                 __syncwarp();
                 if (t + 1 < it.n) {
@@ -753,7 +755,7 @@ bwd_tile_kernel(const __grid_constant__ CUtensorMap tmQx, const __grid_constant_
     BwdCta c;
     c.smem = smem_raw;
     c.sbase = smem_u32(c.smem);
-    c.mask = c.sbase + K::OFF_MASK;
+    c.mask = K::OFF_MASK;
     uint64_t *bars = reinterpret_cast<uint64_t *>(c.smem + K::OFF_BAR);
     c.bar0 = smem_u32(bars);
     volatile int *slot = reinterpret_cast<volatile int *>(bars + K::BARS);  // two items
