@@ -47,10 +47,10 @@
 //
 // Measured on one B200 (the floor: five products of the visible tiles at 1645
 // TFLOP/s; this form's seven take 1.4 times as long):
-//   causal, 2 x 16 heads x 2048 x 128:  124 us in bursts, 141 sustained (floor 52)
+//   causal, 2 x 16 heads x 2048 x 128:  124 us in bursts, 141 to 144 sustained (floor 52)
 //   causal, 32 on 8 heads x 4096 x 128: 436 and 455 (209)
-//   causal, 2 x 16 x 2048, 192 / 128:   175 and 184 (68)
-//   mask, ALiBi, softcap and sinks, 2 x 8 x 1024 x 128: 70 (13)
+//   causal, 2 x 16 x 2048, 192 / 128:   175 and 184 to 190 (68)
+//   mask, ALiBi, softcap and sinks, 2 x 8 x 1024 x 128: 66 (13)
 // The first spends 131 us in the tile kernel under a profiler, its tensor pipe
 // 51 % active, its exponentials' pipe 31 %.  Sustained, the power limit sets
 // the pace: fewer cycles (a second issuing warp, 4 %) bought a lower clock and
@@ -548,7 +548,7 @@ struct BwdWorker {
             // (One form for each set of modifiers: branches inside would keep
             // the columns' chains from overlapping.)
             const auto probabilities = [&](auto capped_, auto masked_) {
-                constexpr bool CAPPED = decltype(capped_)::value, MASKED = decltype(masked_)::value;
+                [[maybe_unused]] constexpr bool CAPPED = decltype(capped_)::value, MASKED = decltype(masked_)::value;
 #pragma unroll
                 for (int i = 0; i < 32; i += 4) {
                     float v[4] = {x[i], x[i + 1], x[i + 2], x[i + 3]};
