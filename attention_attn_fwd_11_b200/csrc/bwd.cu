@@ -79,7 +79,11 @@ struct BwdArgs {
     int B, Hq, Hkv, Sq, Sk, causal;
     float scale, scale_log2;
     ScoreMods mods;
-    const float *nlse, *ndelta;  // -LSE and -D of every row
+    // -LSE and -D of every row.  The row kernel may still be writing them when
+    // the tile kernel starts: read behind its griddepcontrol.wait, with plain
+    // loads (the read-only path promises nothing about data that changes under
+    // a running kernel, and its loads may be moved ahead of the wait).
+    const float *nlse, *ndelta;
     const uint4 *ext;            // the two of a row as the B side of the extra step (see BwdCfg)
     int64_t pitch;               // rows per (batch, head) of the three
     int kv_items, items;          // 128-key tiles of every KV head, then 128-query tiles of every head
@@ -484,8 +488,8 @@ struct BwdWorker {
         float row_nlse = 0.f, row_ndelta = 0.f;
         if (!KV) {  // rows past Sq are padded in the workspace
             const int64_t r = ((int64_t)it.b * a.Hq + it.h) * a.pitch + xr;
-            row_nlse = __ldg(a.nlse + r) * (MODS ? 1.f : kLog2e);
-            row_ndelta = __ldg(a.ndelta + r);
+            row_nlse = a.nlse[r] * (MODS ? 1.f : kLog2e);
+            row_ndelta = a.ndelta[r];
         }
         // dQ: columns c >= lim_hi - y0 of this row are hidden; dK / dV:
         // columns c < lim_lo - y0 of this key.
@@ -732,7 +736,7 @@ FA_DEV void sink_gradients(const BwdArgs &a, int lane) {
         for (int b = 0; b < a.B; ++b) {
             const int64_t r = ((int64_t)b * a.Hq + h) * a.pitch;
 #pragma unroll 4
-            for (int i = lane; i < a.Sq; i += 32) s += ex2((sk + __ldg(a.nlse + r + i)) * kLog2e) * __ldg(a.ndelta + r + i);
+            for (int i = lane; i < a.Sq; i += 32) s += ex2((sk + a.nlse[r + i]) * kLog2e) * a.ndelta[r + i];
         }
 #pragma unroll
         for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
