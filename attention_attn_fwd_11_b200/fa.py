@@ -3,6 +3,10 @@ every step of the computation runs in the library's CUDA kernels.  PyTorch
 supplies device memory and the current stream.  There is no CPU fallback:
 if the library is missing or the tensors are not on a CUDA device, calls
 raise.
+
+A call works on the current stream, or on the one given as ``stream``: the
+caller sees to it that the inputs are ready there, and waits for that stream
+before going on with the results elsewhere.
 """
 from __future__ import annotations
 
@@ -192,19 +196,37 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _stream(stream):
-    if stream is None:  # the current stream's handle, without building a Stream object (3 us)
-        return _vp(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
-    return _vp(stream.cuda_stream)
+def _stream():
+    """The current stream's handle, without building a Stream object (3 us)."""
+    return _vp(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
 
 
-def _used_on(stream, *made):
-    """For tensors made here, on the current stream, whose kernels run on a
-    given one: their memory is not to be handed out before those are done."""
-    if stream is not None:
-        for t in made:
-            if t is not None:
-                t.record_stream(stream)
+def _on(stream, call, *args, **kwargs):
+    """call(*args) with the given stream as the current one, so that what it
+    makes -- outputs, workspaces, temporaries -- comes from that stream's own
+    memory: a block that another stream has freed may still be in use by work
+    queued there, which the given stream does not wait for.  The memory of
+    every tensor given outlasts the kernels, and that of the results also
+    what the caller queues on its own current stream."""
+    before = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        got = call(*args, **kwargs)
+    for t in _tensors((args, tuple(kwargs.values()))):
+        t.record_stream(stream)
+    for t in _tensors(got):
+        t.record_stream(stream)
+        t.record_stream(before)
+    return got
+
+
+def _tensors(x):
+    """The CUDA tensors in x, a tensor or (nested) tuples and lists."""
+    if isinstance(x, torch.Tensor):
+        if x.is_cuda:
+            yield x
+    elif isinstance(x, (tuple, list)):
+        for y in x:
+            yield from _tensors(y)
 
 
 def _need_cuda(*ts):
@@ -267,6 +289,9 @@ def fwd(q, k, v, scale=None, causal=False, out=None, return_lse=True, out_dtype=
     applied to the mask), softcap, sinks [Hq] float32 CUDA tensor.  out and
     lse may be given preallocated (lse: contiguous float32 [B,Hq,Sq]).
     Returns (O [B,Hq,Sq,dv], LSE [B,Hq,Sq] fp32 or None)."""
+    if stream is not None:
+        return _on(stream, fwd, q, k, v, scale, causal, out, return_lse, out_dtype, None, mask, max_bias, softcap,
+                   sinks, lse)
     _need_cuda(q, k, v)
     if mask is not None:
         _need_cuda(mask)
@@ -291,7 +316,7 @@ def fwd(q, k, v, scale=None, causal=False, out=None, return_lse=True, out_dtype=
     elif return_lse:
         lse = torch.empty((B, Hq, Sq), device=q.device, dtype=torch.float32)
     params = fwd_params(q, k, v, out, lse, scale, causal, mask, max_bias, softcap, sinks)
-    _check(load().fa_fwd(ctypes.byref(params), _stream(stream)))
+    _check(load().fa_fwd(ctypes.byref(params), _stream()))
     return out, lse
 
 
@@ -320,6 +345,9 @@ def bwd(q, k, v, o, lse, do, scale=None, causal=False, mask=None, max_bias=0.0, 
     contiguous), else they are made in grad_dtype (bf16 or float32).
     (dk, dv) head sizes: (64, 64), (128, 128), (192, 128).
     Returns (dq, dk, dv), and with sinks (dq, dk, dv, dsinks [Hq] float32)."""
+    if stream is not None:
+        return _on(stream, bwd, q, k, v, o, lse, do, scale, causal, mask, max_bias, softcap, sinks, dlse, dq, dk, dv,
+                   grad_dtype, workspace)
     _need_current_device(q, k, v, o, lse, do, mask, sinks, dlse, dq, dk, dv, workspace)
     bf16 = torch.bfloat16
     if q.dtype != bf16 or k.dtype != bf16 or v.dtype != bf16 or do.dtype != bf16:
@@ -381,8 +409,7 @@ def bwd(q, k, v, o, lse, do, scale=None, causal=False, mask=None, max_bias=0.0, 
         _check(lib.fa_bwd_workspace_size(ref, ctypes.byref(n)))
         workspace = torch.empty(n.value, device=q.device, dtype=torch.uint8)
     p.workspace, p.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _check(lib.fa_bwd(ref, _stream(stream)))
-    _used_on(stream, workspace, dq, dk, dv, dsinks)
+    _check(lib.fa_bwd(ref, _stream()))
     return (dq, dk, dv) if sinks is None else (dq, dk, dv, dsinks)
 
 
@@ -440,6 +467,9 @@ def decode_paged(q, k_cache, v_cache, block_table, seq_lens, scale=None, num_spl
     e4m3 * k_scale / v_scale (dequantised in the kernel); block_table int32
     [B,max_blocks]; seq_lens int32 [B].  Returns (O [B,Hq,dv], LSE [B,Hq] or
     None)."""
+    if stream is not None:
+        return _on(stream, decode_paged, q, k_cache, v_cache, block_table, seq_lens, scale, num_splits, out, return_lse,
+                   out_dtype, workspace, None, kv_type, k_scale, v_scale)
     _need_cuda(q, k_cache, v_cache, block_table, seq_lens)
     B, Hq, dk = q.shape
     if scale is None:
@@ -453,7 +483,7 @@ def decode_paged(q, k_cache, v_cache, block_table, seq_lens, scale=None, num_spl
         workspace = torch.empty(max(n, 256), device=q.device, dtype=torch.uint8)
     p = paged_params(q, k_cache, v_cache, block_table, seq_lens, out, lse, scale, num_splits, workspace, kv_type,
                      k_scale, v_scale)
-    _check(load().fa_decode_paged(ctypes.byref(p), _stream(stream)))
+    _check(load().fa_decode_paged(ctypes.byref(p), _stream()))
     return out, lse
 
 
@@ -495,6 +525,9 @@ def prefill_paged(q, k_cache, v_cache, block_table, seq_lens, scale=None, causal
     Sq, >= max seq_len] float16 (last dim contiguous), max_bias, softcap,
     sinks [Hq] float32: the score modifiers of fwd().
     Returns (O [B,Hq,Sq,dv], LSE [B,Hq,Sq] or None)."""
+    if stream is not None:
+        return _on(stream, prefill_paged, q, k_cache, v_cache, block_table, seq_lens, scale, causal, out, return_lse,
+                   out_dtype, None, q_lens, mask, max_bias, softcap, sinks)
     _need_cuda(mask, sinks)
     if mask is not None and (mask.dtype != torch.float16 or mask.dim() != 4 or mask.stride(3) != 1):
         raise ValueError("mask must be a 4-D float16 tensor with a contiguous last dim")
@@ -518,7 +551,7 @@ def prefill_paged(q, k_cache, v_cache, block_table, seq_lens, scale=None, causal
     lse = torch.empty((B, Hq, Sq), device=q.device, dtype=torch.float32) if return_lse else None
     p = prefill_paged_params(q, k_cache, v_cache, block_table, seq_lens, out, lse, scale, causal, q_lens, mask,
                              max_bias, softcap, sinks)
-    _check(load().fa_prefill_paged(ctypes.byref(p), _stream(stream)))
+    _check(load().fa_prefill_paged(ctypes.byref(p), _stream()))
     return out, lse
 
 
@@ -558,6 +591,9 @@ def decode_gather(q, rows, idx, key_pos=None, q_pos=None, scale=None, num_splits
     ``topk`` given: every token reads rows 0 .. topk - 1; key_pos int32
     [T,topk] or None; q_pos int32 [T] or None.
     Returns (O [T,Hq,512], LSE [T,Hq] or None)."""
+    if stream is not None:
+        return _on(stream, decode_gather, q, rows, idx, key_pos, q_pos, scale, num_splits, out, return_lse, out_dtype,
+                   workspace, None, topk, dk)
     _need_cuda(q, rows, idx, key_pos, q_pos)
     if rows.stride(1) != 1:
         raise ValueError("rows must have a contiguous last dim")
@@ -572,7 +608,7 @@ def decode_gather(q, rows, idx, key_pos=None, q_pos=None, scale=None, num_splits
         workspace = torch.empty(max(n, 256), device=q.device, dtype=torch.uint8)
     p = gather_params(q, rows, idx, key_pos, q_pos, out, lse, scale, num_splits, workspace, topk=topk,
                       dk=dk, v_offset=64 if dk == 576 else 0)
-    _check(load().fa_decode_gather(ctypes.byref(p), _stream(stream)))
+    _check(load().fa_decode_gather(ctypes.byref(p), _stream()))
     return out, lse
 
 
@@ -587,14 +623,16 @@ def prefill_latent(q, rows, causal=True, scale=None, num_splits=0, out=None, ret
     of 512 that are both key and value (q [Sq, 128, 512]).  Runs
     fa_decode_gather with contiguous rows (idx NULL).
     Returns (O [Sq, 128, 512], LSE [Sq, 128])."""
+    if stream is not None:
+        return _on(stream, prefill_latent, q, rows, causal, scale, num_splits, out, return_lse, out_dtype, workspace,
+                   None, dk)
     _need_cuda(q, rows)
     Sq, Sk = q.shape[0], rows.shape[0]
     q_pos = None
     if causal:
         q_pos = torch.arange(Sk - Sq, Sk, device=q.device, dtype=torch.int32)
     return decode_gather(q, rows, None, q_pos=q_pos, scale=scale, num_splits=num_splits, out=out,
-                         return_lse=return_lse, out_dtype=out_dtype, workspace=workspace, stream=stream, topk=Sk,
-                         dk=dk)
+                         return_lse=return_lse, out_dtype=out_dtype, workspace=workspace, topk=Sk, dk=dk)
 
 
 def device_error(clear=True) -> int:
@@ -652,8 +690,10 @@ def kv_dequant(src, qtype, row_elems, out=None, stream=None, kv_scale=1.0):
     ``qtype`` ('q8_0' or 'q4_0' ggml blocks, or 'fp8_e4m3' bytes read as
     e4m3 * kv_scale); the leading dimensions must collapse to one row index
     with a single stride.  Returns (or fills) a bf16 tensor [..., row_elems]."""
+    if stream is not None:
+        return _on(stream, kv_dequant, src, qtype, row_elems, out, None, kv_scale)
     p, out = _dequant_entry(src, qtype, row_elems, out, kv_scale)
-    _check(load().fa_kv_dequant(ctypes.byref(p), _stream(stream)))
+    _check(load().fa_kv_dequant(ctypes.byref(p), _stream()))
     return out
 
 
@@ -661,9 +701,11 @@ def kv_dequant_many(entries, stream=None):
     """Several conversions in one launch (fa_kv_dequant_n).  entries: list of
     (src, qtype, row_elems, out-or-None[, kv_scale]), 1 to 4 of them, one
     qtype.  Returns the list of outputs."""
+    if stream is not None:
+        return _on(stream, kv_dequant_many, entries)
     made = [_dequant_entry(*e) for e in entries]
     arr = (KvDequantParams * len(made))(*[m[0] for m in made])
-    _check(load().fa_kv_dequant_n(arr, len(made), _stream(stream)))
+    _check(load().fa_kv_dequant_n(arr, len(made), _stream()))
     return [m[1] for m in made]
 
 
@@ -675,10 +717,11 @@ def fwd_quant(q, k_blocks, v_blocks, qtype, dk, dv, scale=None, causal=False, ou
     block bytes]; k_buf / v_buf: optional bf16 [B, Hkv, Sk, dk / dv] buffers
     for the dequantised rows (allocated when absent); k_scale / v_scale: the
     fp8 tensor scales.  Other arguments as fwd()."""
-    k, v = kv_dequant_many([(k_blocks, qtype, dk, k_buf, k_scale), (v_blocks, qtype, dv, v_buf, v_scale)],
-                           stream=stream)
-    return fwd(q, k, v, scale=scale, causal=causal, out=out, return_lse=return_lse, out_dtype=out_dtype,
-               stream=stream, **mods)
+    if stream is not None:
+        return _on(stream, fwd_quant, q, k_blocks, v_blocks, qtype, dk, dv, scale, causal, out, return_lse, out_dtype,
+                   k_buf, v_buf, None, k_scale, v_scale, **mods)
+    k, v = kv_dequant_many([(k_blocks, qtype, dk, k_buf, k_scale), (v_blocks, qtype, dv, v_buf, v_scale)])
+    return fwd(q, k, v, scale=scale, causal=causal, out=out, return_lse=return_lse, out_dtype=out_dtype, **mods)
 
 
 # --------------------------------------------------------- MLA decode tail --
@@ -709,6 +752,8 @@ def mla_tail(o_lat, w_abs, w_o, out=None, out_dtype=torch.float32, num_splits=0,
     """MLA decode tail (fa_mla_tail): y [T, Hd] = o-projection of the
     per-head out-absorb of o_lat [T, Hq, R].  w_abs [Hq, V, R]; w_o
     [Hd, Hq*V] (row = output feature).  All bf16, contiguous."""
+    if stream is not None:
+        return _on(stream, mla_tail, o_lat, w_abs, w_o, out, out_dtype, num_splits, workspace)
     _need_cuda(o_lat, w_abs, w_o, out, workspace)
     for t in (o_lat, w_abs, w_o):
         if t.dtype != torch.bfloat16 or not t.is_contiguous():
@@ -720,7 +765,7 @@ def mla_tail(o_lat, w_abs, w_o, out=None, out_dtype=torch.float32, num_splits=0,
         n = mla_tail_workspace_bytes(o_lat, w_abs, w_o, num_splits)
         workspace = torch.empty(max(n, 256), device=o_lat.device, dtype=torch.uint8)
     p = mla_tail_params(o_lat, w_abs, w_o, out, num_splits, workspace)
-    _check(load().fa_mla_tail(ctypes.byref(p), _stream(stream)))
+    _check(load().fa_mla_tail(ctypes.byref(p), _stream()))
     return out
 
 
@@ -790,6 +835,8 @@ def rope(q, inv_freq, k=None, pos=None, pos0=0, interleaved=False, offset=0, inv
     dim.  pos: int32 CUDA tensor [S], [1,S] or [B,S], or None: row s is at
     pos0 + s.  inverse=True turns back: the gradient.  out / k_out may be
     given, also as q / k themselves.  Returns (q turned, k turned or None)."""
+    if stream is not None:
+        return _on(stream, rope, q, inv_freq, k, pos, pos0, interleaved, offset, inverse, mscale, out, k_out)
     _need_current_device(q, k, pos, out, k_out)
     dtype, qs = q.dtype, q.shape
     if (dtype != torch.bfloat16 and dtype != torch.float32) or len(qs) != 4:
@@ -820,8 +867,7 @@ def rope(q, inv_freq, k=None, pos=None, pos0=0, interleaved=False, offset=0, inv
     p = _pack_rope(q.data_ptr(), out.data_ptr(), q0, q1, q2, o0, o1, o2, k_in, k_made, k0, k1, k2, r0, r1, r2, B, Hq, Hk,
                    S, d, _odt(dtype), pos_in, pos_sb, pos0, inv_freq.data_ptr(), 2 * inv_freq.numel(), offset,
                    1 if interleaved else 0, 1 if inverse else 0, mscale)
-    _check(load().fa_rope(ctypes.byref(p), _stream(stream)))
-    _used_on(stream, out, k_out)
+    _check(load().fa_rope(ctypes.byref(p), _stream()))
     return out, k_out
 
 
@@ -838,6 +884,9 @@ def kv_append(k, v, k_cache, v_cache, block_table, seq_lens, q_lens=None, inv_fr
     pos (int32 [B,Sq], [1,Sq] or [Sq]) or else the row's place in its
     sequence; q [B,Hq,Sq,dk], if given, is turned too.  Returns q turned (in
     q_out, which may be q; rows past q_lens are zeros), or None without q."""
+    if stream is not None:
+        return _on(stream, kv_append, k, v, k_cache, v_cache, block_table, seq_lens, q_lens, inv_freq, mscale, pos,
+                   interleaved, offset, q, q_out, kv_type, k_scale, v_scale)
     _need_current_device(k, v, k_cache, v_cache, block_table, seq_lens, q_lens, q, q_out, pos)
     bf16, ks, vs, cs, cvs, ctype = torch.bfloat16, k.shape, v.shape, k_cache.shape, v_cache.shape, k_cache.dtype
     k0, k1, k2, k3 = k.stride() if len(ks) == 4 else (0, 0, 0, 0)
@@ -890,6 +939,5 @@ def kv_append(k, v, k_cache, v_cache, block_table, seq_lens, q_lens=None, inv_fr
         p.q_sb, p.q_sh, p.q_ss, p.qo_sb, p.qo_sh, p.qo_ss = q0, q1, q2, o0, o1, o2
     elif q_out is not None:
         raise ValueError("q_out without q")
-    _check(load().fa_kv_append(ctypes.byref(p), _stream(stream)))
-    _used_on(stream, q_out)
+    _check(load().fa_kv_append(ctypes.byref(p), _stream()))
     return q_out
