@@ -14,6 +14,7 @@
 
 #include "../../include/fa.h"
 #include "internal.h"
+#include "overlap.h"
 
 namespace {
 
@@ -359,7 +360,15 @@ fa_status check_rows(const char *who, const char *name, const void *src, int64_t
     if (!aligned16(src)) return fail(FA_ERR_INVALID_ARG, "%s: %s must be 16-byte aligned", who, name);
     if ((B > 1 && sb % unit) || (H > 1 && sh % unit) || (S > 1 && ss % unit))
         return fail(FA_ERR_INVALID_ARG, "%s: %s strides must be multiples of %d elements", who, name, unit);
+    constexpr int64_t far = int64_t(1) << 40;
+    if ((B > 1 && (sb > far || sb < -far)) || (H > 1 && (sh > far || sh < -far)) || (S > 1 && (ss > far || ss < -far)))
+        return fail(FA_ERR_INVALID_ARG, "%s: %s strides out of range", who, name);
     return FA_OK;
+}
+
+// What such a tensor covers (strides in elements of `bytes` bytes).
+fa::Rows byte_rows(const void *p, int64_t sb, int64_t sh, int64_t ss, int B, int H, int S, int d, int bytes) {
+    return fa::Rows{p, (int64_t)d * bytes, {B, H, S}, {sb * bytes, sh * bytes, ss * bytes}};
 }
 
 fa_status rope_tensor(const char *who, const char *name, const void *src, void *dst, int64_t sb, int64_t sh,
@@ -368,11 +377,14 @@ fa_status rope_tensor(const char *who, const char *name, const void *src, void *
     fa_status st = check_rows(who, name, src, sb, sh, ss, B, H, S, unit);
     if (st == FA_OK) st = check_rows(who, name, dst, ob, oh, os, B, H, S, unit);
     if (st != FA_OK) return st;
-    if ((B > 1 && ob == 0) || (H > 1 && oh == 0) || (S > 1 && os > -d && os < d))
-        return fail(FA_ERR_INVALID_ARG, "%s: the rows of %s's output overlap", who, name);
     const bool same = (B == 1 || sb == ob) && (H == 1 || sh == oh) && (S == 1 || ss == os);
+    const int bytes = 16 / unit;
+    const fa::Rows to = byte_rows(dst, ob, oh, os, B, H, S, d, bytes);
+    if (fa::rows_meet_themselves(to)) return fail(FA_ERR_INVALID_ARG, "%s: the rows of %s's output overlap", who, name);
     if (src == dst && !same)
         return fail(FA_ERR_INVALID_ARG, "%s: %s turned in place needs equal strides", who, name);
+    if (src != dst && fa::rows_meet(to, byte_rows(src, sb, sh, ss, B, H, S, d, bytes)))
+        return fail(FA_ERR_INVALID_ARG, "%s: %s's output and its input overlap and are not the same rows", who, name);
     *t = fa::RopeTensor{src, dst, H, sb, sh, ss, ob, oh, os, src == dst};
     return FA_OK;
 }
@@ -962,6 +974,15 @@ fa_status fa_rope(const fa_rope_params *p, void *stream) {
         st = rope_tensor(who, "k", p->k, p->k_out, p->k_sb, p->k_sh, p->k_ss, p->ko_sb, p->ko_sh, p->ko_ss, p->B,
                          p->Hk, p->S, p->d, unit, &L.x[1]);
     if (st != FA_OK) return st;
+    if (p->Hk > 0) {  // one launch reads and writes all four
+        const int bytes = 16 / unit;
+        const fa::Rows q = byte_rows(p->q, p->q_sb, p->q_sh, p->q_ss, p->B, p->Hq, p->S, p->d, bytes),
+                       k = byte_rows(p->k, p->k_sb, p->k_sh, p->k_ss, p->B, p->Hk, p->S, p->d, bytes),
+                       qo = byte_rows(p->q_out, p->qo_sb, p->qo_sh, p->qo_ss, p->B, p->Hq, p->S, p->d, bytes),
+                       ko = byte_rows(p->k_out, p->ko_sb, p->ko_sh, p->ko_ss, p->B, p->Hk, p->S, p->d, bytes);
+        if (fa::rows_meet(qo, ko) || fa::rows_meet(qo, k) || fa::rows_meet(ko, q))
+            return fail(FA_ERR_INVALID_ARG, "fa_rope: each output must be apart from the other and from the other's input");
+    }
     L.B = p->B;
     L.S = p->S;
     L.d = p->d;
@@ -1025,6 +1046,24 @@ fa_status fa_kv_append(const fa_kv_append_params *p, void *stream) {
         return fail(FA_ERR_INVALID_ARG, "fa_kv_append: the caches must be 16-byte aligned");
     if (((uintptr_t)p->block_table & 3u) || ((uintptr_t)p->seq_lens & 3u) || ((uintptr_t)p->q_lens & 3u))
         return fail(FA_ERR_INVALID_ARG, "fa_kv_append: block_table, seq_lens and q_lens must be 4-byte aligned");
+    {
+        const auto cache = [&](const void *c, int d) {
+            const int64_t row = p->kv_type == FA_KV_BF16   ? 2 * d
+                                : p->kv_type == FA_KV_Q8_0 ? d / 32 * 34
+                                : p->kv_type == FA_KV_Q4_0 ? d / 32 * 18
+                                                           : d;
+            return fa::Rows{c, (int64_t)p->Hkv * 64 * row, {p->num_blocks, 1, 1}, {(int64_t)p->Hkv * 64 * row, 0, 0}};
+        };
+        const fa::Rows kc = cache(p->k_cache, p->dk), vc = cache(p->v_cache, p->dv);
+        if (fa::rows_meet(kc, vc)) return fail(FA_ERR_INVALID_ARG, "fa_kv_append: the caches overlap");
+        if (Hq > 0) {
+            const fa::Rows to = byte_rows(p->q_out, p->qo_sb, p->qo_sh, p->qo_ss, p->B, Hq, p->Sq, p->dk, 2);
+            if (fa::rows_meet(to, kc) || fa::rows_meet(to, vc) ||
+                fa::rows_meet(to, byte_rows(p->k, p->k_sb, p->k_sh, p->k_ss, p->B, p->Hkv, p->Sq, p->dk, 2)) ||
+                fa::rows_meet(to, byte_rows(p->v, p->v_sb, p->v_sh, p->v_ss, p->B, p->Hkv, p->Sq, p->dv, 2)))
+                return fail(FA_ERR_INVALID_ARG, "fa_kv_append: q_out must be apart from k, v and the caches");
+        }
+    }
     L.k = fa::RopeTensor{p->k, p->k_cache, p->Hkv, p->k_sb, p->k_sh, p->k_ss, 0, 0, 0, 0};
     L.v = fa::RopeTensor{p->v, p->v_cache, p->Hkv, p->v_sb, p->v_sh, p->v_ss, 0, 0, 0, 0};
     L.block_table = p->block_table;

@@ -499,8 +499,10 @@ fa_status fa_decode_gather(const fa_decode_gather_params *p, void *stream);
  * gradient of x.
  *   q: [B, Hq, S, d] (dtype: FA_BF16 or FA_F32), k: [B, Hk, S, d] or absent
  *     (k NULL, Hk 0).  q_out, k_out: the same shapes and dtype; each may be
- *     its input (same strides) and may not overlap it otherwise.  The result
- *     is computed in fp32 and rounded once.
+ *     its input (same strides).  Otherwise an output's rows may share memory
+ *     neither with one another nor with any other row of the call (q, k,
+ *     q_out, k_out may be views of one buffer whose rows lie beside one
+ *     another).  The result is computed in fp32 and rounded once.
  *   Strides (elements) give batch / head / sequence steps, multiples of 8
  *     for bf16 and 4 for fp32 (an input's may be 0); base pointers 16-byte
  *     aligned.
@@ -573,6 +575,9 @@ fa_status fa_rope(const fa_rope_params *p, void *stream);
  * A place past the table's end, or a block id outside [0, num_blocks), is
  * latched as FA_DEVERR_BAD_BLOCK and the row is not written.  No two new rows
  * may share a slot (a block that two sequences' tables name for new rows).
+ * The caches may not overlap each other, nor q_out's rows k, v, the caches or
+ * (but for q_out = q) q; rows of k, v and q may lie in the caches only outside
+ * the slots that are written.
  * B == 0 or Sq == 0 is a no-op.
  */
 typedef struct {
