@@ -445,6 +445,43 @@ fa_status check_grad(const char *name, const void *g, int64_t sb, int64_t sh, in
     return FA_OK;
 }
 
+// What fa_bwd writes -- the gradients, the sinks' gradient, the workspace --
+// against all that it reads and one another.
+fa_status check_bwd_apart(const fa_bwd_params *p, bool rows, bool keys, size_t ws_bytes) {
+    struct Named {
+        const char *name;
+        fa::Rows r;
+    } x[15];
+    int n = 0;
+    const auto put = [&](const char *name, const void *t, int64_t sb, int64_t sh, int64_t ss, int H, int S, int d, int bytes) {
+        if (t && p->B > 0 && S > 0) x[n++] = Named{name, byte_rows(t, sb, sh, ss, p->B, H, S, d, bytes)};
+    };
+    const auto flat = [&](const char *name, const void *t, int64_t bytes) {
+        if (t && bytes > 0) x[n++] = Named{name, fa::Rows{t, bytes, {1, 1, 1}, {0, 0, 0}}};
+    };
+    const int gb = p->g_dtype == FA_F32 ? 4 : 2, Sq = rows ? p->Sq : 0, Sk = keys ? p->Sk : 0;
+    put("gq", p->gq, p->gq_sb, p->gq_sh, p->gq_ss, p->Hq, Sq, p->dk, gb);
+    put("gk", p->gk, p->gk_sb, p->gk_sh, p->gk_ss, p->Hkv, Sk, p->dk, gb);
+    put("gv", p->gv, p->gv_sb, p->gv_sh, p->gv_ss, p->Hkv, Sk, p->dv, gb);
+    flat("gsinks", p->gsinks, 4 * (int64_t)p->Hq);
+    flat("the workspace", p->workspace, (int64_t)ws_bytes);
+    const int written = n;
+    put("q", p->q, p->q_sb, p->q_sh, p->q_ss, p->Hq, Sq, p->dk, 2);
+    put("k", p->k, p->k_sb, p->k_sh, p->k_ss, p->Hkv, Sk, p->dk, 2);
+    put("v", p->v, p->v_sb, p->v_sh, p->v_ss, p->Hkv, Sk, p->dv, 2);
+    put("o", p->o, p->o_sb, p->o_sh, p->o_ss, p->Hq, Sq, p->dv, p->o_dtype == FA_F32 ? 4 : 2);
+    put("dout", p->dout, p->do_sb, p->do_sh, p->do_ss, p->Hq, Sq, p->dv, 2);
+    flat("lse", p->lse, 4 * (int64_t)p->B * p->Hq * Sq);
+    flat("dlse", p->dlse, 4 * (int64_t)p->B * p->Hq * Sq);
+    flat("sinks", p->sinks, 4 * (int64_t)p->Hq);
+    if (Sk > 0) put("mask", p->mask, p->m_sb, p->m_sh, p->m_ss, p->Hq, Sq, Sk, 2);
+    for (int i = 0; i < written; ++i)
+        for (int j = i + 1; j < n; ++j)
+            if (fa::rows_meet(x[i].r, x[j].r))
+                return fail(FA_ERR_INVALID_ARG, "fa_bwd: %s must be apart from %s", x[i].name, x[j].name);
+    return FA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1138,6 +1175,8 @@ fa_status fa_bwd(const fa_bwd_params *p, void *stream) {
     const size_t each = bwd_row_bytes(p), need = bwd_bytes(p, p->causal != 0);
     if (!p->workspace || p->workspace_bytes < need || ((uintptr_t)p->workspace & 255u))
         return fail(FA_ERR_WORKSPACE, "fa_bwd: workspace needs %zu bytes, 256-byte aligned", need);
+    st = check_bwd_apart(p, rows, keys, need);
+    if (st != FA_OK) return st;
     if (!get_encoder()) return fail(FA_ERR_CUDA, "fa_bwd: cuTensorMapEncodeTiled is not available");
     fa::BwdLaunch L;
     memset(&L, 0, sizeof L);

@@ -74,8 +74,19 @@ struct Equation {  // sum of x_k step_k + offset within [low, high], lo_k <= x_k
 
 }  // namespace overlap_detail
 
+// First byte and the one behind the last.
+inline void rows_span(const Rows &a, overlap_detail::wide *first, overlap_detail::wide *end) {
+    *first = *end = (overlap_detail::wide)(uintptr_t)a.p;
+    for (int k = 0; k < 3; ++k) *(a.step[k] < 0 ? first : end) += (overlap_detail::wide)(a.n[k] - 1) * a.step[k];
+    *end += a.width;
+}
+
 // Some byte belongs to both (or 20000 tries did not settle it).
 inline bool rows_meet(const Rows &a, const Rows &b) {
+    overlap_detail::wide a0, a1, b0, b1;
+    rows_span(a, &a0, &a1);
+    rows_span(b, &b0, &b1);
+    if (a1 <= b0 || b1 <= a0) return false;  // nearly always
     overlap_detail::Equation e;
     e.low = 1 - b.width, e.high = a.width - 1;
     for (int k = 0; k < 3; ++k) {

@@ -157,8 +157,10 @@ fa_status fa_fwd(const fa_fwd_params *p, void *stream);
  *     g_dtype, strides multiples of 8 (bf16) or 4 (fp32), bases 16-byte
  *     aligned, the three dimensions nested in any order (each stride at least
  *     the extent of those inside it; extents of 1 take any stride).  A KV
- *     head's gradients are the sums over its query heads.  They may overlap
- *     neither the inputs nor one another.
+ *     head's gradients are the sums over its query heads.  What is written
+ *     (gq, gk, gv, gsinks, the workspace) may share memory neither with one
+ *     another nor with anything that is read; views of one buffer whose rows
+ *     lie beside one another are fine.
  *   gsinks: NULL, or [Hq] fp32 (needs sinks): the gradient of the sinks,
  *     -sum over rows of exp(sink_h - lse) D.
  *   Rows with no visible key (lse -inf) get gq = 0 and add nothing.  There is
