@@ -229,6 +229,15 @@ def _tensors(x):
             yield from _tensors(y)
 
 
+def _workspace(ws):
+    """(address, bytes) of a workspace tensor."""
+    if ws is None:
+        return None, 0
+    if not ws.is_contiguous():  # its elements would not fill the bytes from its address on
+        raise ValueError("the workspace must be contiguous")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
 def _need_cuda(*ts):
     for t in ts:
         if t is not None and not t.is_cuda:
@@ -408,7 +417,7 @@ def bwd(q, k, v, o, lse, do, scale=None, causal=False, mask=None, max_bias=0.0, 
         n = ctypes.c_size_t(0)
         _check(lib.fa_bwd_workspace_size(ref, ctypes.byref(n)))
         workspace = torch.empty(n.value, device=q.device, dtype=torch.uint8)
-    p.workspace, p.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    p.workspace, p.workspace_bytes = _workspace(workspace)
     _check(lib.fa_bwd(ref, _stream()))
     return (dq, dk, dv) if sinks is None else (dq, dk, dv, dsinks)
 
@@ -446,8 +455,7 @@ def paged_params(q, k_cache, v_cache, block_table, seq_lens, o, lse, scale, num_
     p.num_splits = num_splits
     p.o, p.lse = _ptr(o), _ptr(lse)
     p.o_dtype = _odt(o.dtype) if o is not None else FA_F32
-    p.workspace = _ptr(ws)
-    p.workspace_bytes = 0 if ws is None else ws.numel() * ws.element_size()
+    p.workspace, p.workspace_bytes = _workspace(ws)
     return p
 
 
@@ -470,7 +478,7 @@ def decode_paged(q, k_cache, v_cache, block_table, seq_lens, scale=None, num_spl
     if stream is not None:
         return _on(stream, decode_paged, q, k_cache, v_cache, block_table, seq_lens, scale, num_splits, out, return_lse,
                    out_dtype, workspace, None, kv_type, k_scale, v_scale)
-    _need_cuda(q, k_cache, v_cache, block_table, seq_lens)
+    _need_cuda(q, k_cache, v_cache, block_table, seq_lens, out, workspace)
     B, Hq, dk = q.shape
     if scale is None:
         scale = 1.0 / math.sqrt(dk)
@@ -571,8 +579,7 @@ def gather_params(q, rows, idx, key_pos, q_pos, o, lse, scale, num_splits, ws, d
     p.num_splits = num_splits
     p.o, p.lse = _ptr(o), _ptr(lse)
     p.o_dtype = _odt(o.dtype) if o is not None else FA_F32
-    p.workspace = _ptr(ws)
-    p.workspace_bytes = 0 if ws is None else ws.numel() * ws.element_size()
+    p.workspace, p.workspace_bytes = _workspace(ws)
     return p
 
 
@@ -594,7 +601,7 @@ def decode_gather(q, rows, idx, key_pos=None, q_pos=None, scale=None, num_splits
     if stream is not None:
         return _on(stream, decode_gather, q, rows, idx, key_pos, q_pos, scale, num_splits, out, return_lse, out_dtype,
                    workspace, None, topk, dk)
-    _need_cuda(q, rows, idx, key_pos, q_pos)
+    _need_cuda(q, rows, idx, key_pos, q_pos, out, workspace)
     if rows.stride(1) != 1:
         raise ValueError("rows must have a contiguous last dim")
     T, Hq, dk = q.shape
@@ -733,8 +740,7 @@ def mla_tail_params(o_lat, w_abs, w_o, y, num_splits=0, workspace=None):
     p.T, p.Hq, p.R, p.V, p.Hd = T, Hq, R, w_abs.shape[1], w_o.shape[0]
     p.y_dtype = _odt(y.dtype)
     p.num_splits = num_splits
-    p.workspace = _ptr(workspace)
-    p.workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    p.workspace, p.workspace_bytes = _workspace(workspace)
     return p
 
 
