@@ -128,6 +128,13 @@ def _packer(cls, n):
     return make
 
 
+def _int(x):
+    """x for an int field set by name: ctypes would keep its lowest 32 bits without a word."""
+    if not -(1 << 31) <= x < 1 << 31:
+        raise ValueError("an argument is out of its type's range: %d" % x)
+    return x
+
+
 _pack_bwd, _pack_rope, _pack_append = _packer(BwdParams, 45), _packer(RopeParams, 31), _packer(KvAppendParams, 22)
 
 FA_KV_Q8_0, FA_KV_Q4_0, FA_KV_FP8_E4M3 = 8, 4, 2
@@ -333,8 +340,8 @@ def fwd(q, k, v, scale=None, causal=False, out=None, return_lse=True, out_dtype=
 
 def _bwd_sizes(q, k, v):
     p = BwdParams()
-    p.B, p.Hq, p.Sq, p.dk = q.shape
-    p.Hkv, p.Sk, p.dv = v.shape[1:]
+    p.B, p.Hq, p.Sq, p.dk = map(_int, q.shape)
+    p.Hkv, p.Sk, p.dv = map(_int, v.shape[1:])
     p.scale = 1.0
     return p
 
@@ -925,8 +932,8 @@ def kv_append(k, v, k_cache, v_cache, block_table, seq_lens, q_lens=None, inv_fr
     p.mscale = mscale
     if inv_freq is not None:
         _check_inv_freq(inv_freq)
-        p.inv_freq, p.rot_dim, p.rot_offset = inv_freq.data_ptr(), 2 * inv_freq.numel(), offset
-        p.interleaved = int(interleaved)
+        p.inv_freq, p.rot_dim, p.rot_offset = inv_freq.data_ptr(), _int(2 * inv_freq.numel()), _int(offset)
+        p.interleaved = 1 if interleaved else 0
     if pos is not None:
         p.pos_sb, p.pos = _check_pos(pos, B, Sq), pos.data_ptr()
     if q is not None:
@@ -941,7 +948,7 @@ def kv_append(k, v, k_cache, v_cache, block_table, seq_lens, q_lens=None, inv_fr
         o0, o1, o2, o3 = q_out.stride()
         if q_out.shape != qs or q_out.dtype != bf16 or q3 != 1 or o3 != 1:
             raise ValueError("q_out must have q's shape and dtype, and both a contiguous last dim")
-        p.q, p.q_out, p.Hq = q.data_ptr(), q_out.data_ptr(), qs[1]
+        p.q, p.q_out, p.Hq = q.data_ptr(), q_out.data_ptr(), _int(qs[1])
         p.q_sb, p.q_sh, p.q_ss, p.qo_sb, p.qo_sh, p.qo_ss = q0, q1, q2, o0, o1, o2
     elif q_out is not None:
         raise ValueError("q_out without q")
