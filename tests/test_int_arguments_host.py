@@ -11,7 +11,8 @@ from attention_attn_fwd_11_b200 import fa
 def launched(monkeypatch):
     """The parameters of the calls that reach the library, which is not there."""
     got = []
-    monkeypatch.setattr(fa, "load", lambda: types.SimpleNamespace(fa_kv_append=lambda p, s: got.append(p._obj) or fa.FA_OK))
+    call = lambda p, *a: got.append(p._obj) or fa.FA_OK  # noqa: E731
+    monkeypatch.setattr(fa, "load", lambda: types.SimpleNamespace(fa_kv_append=call, fa_bwd_workspace_size=call))
     monkeypatch.setattr(fa, "_need_current_device", lambda *a: None)
     monkeypatch.setattr(fa, "_stream", lambda *a: None)
     return got
