@@ -834,7 +834,7 @@ def _check_inv_freq(inv_freq):
 
 def _check_pos(pos, B, S):
     """Pitch of pos over the batch (0 broadcasts)."""
-    if pos.dtype != torch.int32 or (S > 1 and pos.stride(-1) != 1) or pos.shape not in ((B, S), (S,), (1, S)):
+    if pos.dtype != torch.int32 or pos.shape not in ((B, S), (S,), (1, S)) or (S > 1 and pos.stride(-1) != 1):
         raise ValueError("pos must be an int32 tensor [S], [1, S] or [B, S] with a contiguous last dim")
     return pos.stride(0) if pos.dim() == 2 and pos.shape[0] > 1 else 0
 
