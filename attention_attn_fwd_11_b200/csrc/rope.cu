@@ -13,9 +13,11 @@
 // Angles: p f_i in fp32 would be off by p f_i 2^-24 radians, which is 0.06 at
 // a million tokens.  The host turns f_i into a 64-bit fraction of a turn,
 // t_i = f_i / (2 pi) mod 1, so that p t_i mod 2^64 -- one integer product,
-// whose overflow drops the whole turns -- is the exact fraction of the turn
-// that the position has reached.  Its upper 32 bits (1.5e-9 radians) go to
-// sincospif.
+// whose overflow drops the whole turns -- is the fraction of the turn that the
+// position has reached: within 3 p 2^-64 turns for f_i up to 2 pi, 2.2e-9
+// radians at p = 2^31.  Its upper 32 bits (1.5e-9 radians) go to sincospif,
+// less the nearest quarter turn, as fp32 (2.4e-8): together within 2.8e-8
+// radians.
 //
 // Both kernels move each row once and are bound by HBM.  A thread owns an
 // item of two 16-byte vectors: their pairs, or columns that pass through.
@@ -50,9 +52,18 @@ template <int V>
 FA_DEV void item_angles(const RopeMap &r, int i, int pos, float (&c)[V], float (&s)[V]) {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const uint64_t t = r.turns[V * i + j] * (uint64_t)(int64_t)pos;
-        const float half_turns = (float)(int32_t)(uint32_t)(t >> 32) * 0x1p-31f;  // in [-1, 1]
-        sincospif(half_turns, &s[j], &c[j]);
+        const uint32_t t = (uint32_t)(r.turns[V * i + j] * (uint64_t)(int64_t)pos >> 32);
+        // The nearest quarter turn comes off in whole numbers, so that fp32
+        // holds what is left (an eighth of a turn at most) to 2.4e-8 radians;
+        // the whole turn's fraction would be rounded by up to 9.4e-8.
+        const uint32_t quarters = (t + 0x20000000u) >> 30;
+        const float half_turns = (float)(int32_t)(t - (quarters << 30)) * 0x1p-31f;  // in [-1/4, 1/4]
+        float sn, cn;
+        sincospif(half_turns, &sn, &cn);
+        s[j] = quarters & 1 ? cn : sn;
+        c[j] = quarters & 1 ? sn : cn;
+        if (quarters & 2) s[j] = -s[j];
+        if ((quarters + 1) & 2) c[j] = -c[j];
         c[j] *= r.mscale;
         s[j] *= r.inverse ? -r.mscale : r.mscale;
     }

@@ -510,8 +510,8 @@ fa_status fa_decode_gather(const fa_decode_gather_params *p, void *stream);
  *     aligned.
  *   inv_freq: rot_dim / 2 angular frequencies (radians per position) in HOST
  *     memory, finite, read during the call.  Any scaling for long contexts is
- *     in them and in mscale (finite).  The angles are exact to 1.5e-9 radians
- *     at any position.
+ *     in them and in mscale (finite).  The angles are within 2.8e-8 radians at
+ *     any position (frequencies above 2 pi: 2.4e-10 more for each radian).
  *   Columns [rot_offset, rot_offset + rot_dim) are rotated, the others are
  *     copied (left alone where the output is the input).  Pair i is columns
  *     (i, i + rot_dim / 2) of them, or with interleaved != 0 (2i, 2i + 1).
