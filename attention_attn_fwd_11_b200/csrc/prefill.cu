@@ -84,7 +84,13 @@ struct PrefillCfg {
 };
 
 // Barrier slots (uint64 each).
-enum { B_QFULL = 0, B_DRAIN = 1, B_SFULL = 2, B_PREADY = 4, B_PVDONE = 6, B_RING = 7 };
+// PV of tile t completes B_PVDONE + (t & 1).  Softmax waits for it only where it
+// must, and a wait's parity tells a phase from its neighbours alone: the phase
+// before must be over.  With two barriers that is PV of tile t - 2, behind which
+// S of tile t, seen by then, was issued.  (With one it was PV of tile t - 1: the
+// epilogue of a walk without a rescale could pass while that still waited for
+// its V, and read O half done.)
+enum { B_QFULL = 0, B_DRAIN = 1, B_SFULL = 2, B_PREADY = 4, B_PVDONE = 6, B_RING = 8 };
 
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: rescale when the max grows by > 2^8
 
@@ -139,6 +145,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         mbar_init(bar(B_PREADY), 128);
         mbar_init(bar(B_PREADY + 1), 128);
         mbar_init(bar(B_PVDONE), 1);
+        mbar_init(bar(B_PVDONE + 1), 1);
         for (int s = 0; s < NST; ++s) {
             mbar_init(k_full(s), 1);
             mbar_init(k_empty(s), 1);
@@ -250,7 +257,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                     mma_ts4_warp<8, (2048 >> 4)>(tO, tP + (uint32_t)(kb * 8), bd0 + (uint64_t)(kb * (2048 >> 4)),
                                                  idesc_pv, (t > 0 || kb > 0) ? 1u : 0u);
                 mma_commit_warp(v_empty(s));
-                mma_commit_warp(bar(B_PVDONE));
+                mma_commit_warp(bar(B_PVDONE + (t & 1)));
             }
             // Nothing of ours may still run on the tensor core once TMEM is freed.
             mma_commit_warp(bar(B_DRAIN));
@@ -328,7 +335,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             }
             if (t > 0 && __any_sync(0xffffffffu, need)) {
                 // O must hold PV of tile t-1 before it is rescaled.
-                if (!mbar_wait(bar(B_PVDONE), (uint32_t)(t - 1) & 1u, abort_flag, &g_prefill_err)) {
+                if (!mbar_wait(bar(B_PVDONE + ((t - 1) & 1)), (uint32_t)((t - 1) >> 1) & 1u, abort_flag, &g_prefill_err)) {
                     ok = false;
                     break;
                 }
@@ -372,7 +379,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         // ---- epilogue: O / l, LSE ----
         bool have_o = ok && n_tiles > 0;
         if (have_o) {
-            if (mbar_wait(bar(B_PVDONE), (uint32_t)(n_tiles - 1) & 1u, abort_flag, &g_prefill_err))
+            if (mbar_wait(bar(B_PVDONE + ((n_tiles - 1) & 1)), (uint32_t)((n_tiles - 1) >> 1) & 1u, abort_flag, &g_prefill_err))
                 tc_fence_after();
             else
                 have_o = false;
