@@ -78,6 +78,7 @@ struct BwdGrad {  // an output [B, H, S, d]
 struct BwdArgs {
     int B, Hq, Hkv, Sq, Sk, causal;
     float scale, scale_log2;
+    float grad_scale;  // of dQ and dK: the scale, times what softcap4_slope leaves out
     ScoreMods mods;
     // -LSE and -D of every row.  The row kernel may still be writing them when
     // the tile kernel starts: read behind its griddepcontrol.wait, with plain
@@ -484,7 +485,6 @@ struct BwdWorker {
         const int shift = a.Sk - a.Sq;
         const bool capped = MODS && a.mods.softcap != 0.f;
         const bool masked = MODS && a.mods.mask != nullptr;
-        const float root = capped ? rsqrtf(a.mods.softcap) / kLog2e : 0.f;  // v root = sqrt(softcap) tanh
         float row_nlse = 0.f, row_ndelta = 0.f;
         if (!KV) {  // rows past Sq are padded in the workspace
             const int64_t r = ((int64_t)it.b * a.Hq + it.h) * a.pitch + xr;
@@ -547,7 +547,7 @@ struct BwdWorker {
                 cp_async_wait<0>();
                 __syncwarp();
             }
-            // P (and under a softcap P ds/dz in its place in x)
+            // P (and under a softcap P ds/dz / (4 softcap) in its place in x)
             uint32_t pk[16];
             // (One form for each set of modifiers: branches inside would keep
             // the columns' chains from overlapping.)
@@ -571,15 +571,7 @@ struct BwdWorker {
                     }
                     if constexpr (MODS) {
                         if constexpr (CAPPED) {
-                            // softcap (1 - tanh^2), as softcap - (v root)^2
-                            softcap4(v, a.scale, a.mods.softcap);
-#pragma unroll
-                            for (int j = 0; j < 4; j += 2) {
-                                const uint64_t w = f2_pack(v[j], v[j + 1]);
-                                f2_unpack(f2_fma(f2_mul(w, f2_pack(-root, -root)), f2_mul(w, f2_pack(root, root)),
-                                                 f2_pack(a.mods.softcap, a.mods.softcap)),
-                                          cap[j], cap[j + 1]);
-                            }
+                            softcap4_slope(v, cap, a.scale, a.mods.softcap);
                         } else {
 #pragma unroll
                             for (int j = 0; j < 4; ++j) v[j] *= a.scale_log2;
@@ -721,7 +713,7 @@ struct BwdWorker {
                 for (int i = 0; i < 32; ++i) r[i] = 0u;
             }
             store_rows(KV ? (second ? a.gv : a.gk) : a.gq, a.g_bf16, it.b, it.h, row0, S, second ? col - DK : col, r,
-                       second ? 1.f : a.scale, lane);
+                       second ? 1.f : a.grad_scale, lane);
         }
         return true;
     }
@@ -940,7 +932,7 @@ __global__ void __launch_bounds__(512) bwd_join_kernel(const BwdArgs a, int kv_b
         const int S = KV ? a.Sk : a.Sq;
         if (group > 0 || it.x0 + row >= S) return;
         const bool second = col >= DK;
-        const float f = second ? 1.f : a.scale;
+        const float f = second ? 1.f : a.grad_scale;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
 #pragma unroll
@@ -1202,6 +1194,7 @@ cudaError_t launch_bwd(const BwdLaunch &L, int num_sms, cudaStream_t stream) {
     a.B = L.B, a.Hq = L.Hq, a.Hkv = L.Hkv, a.Sq = L.Sq, a.Sk = L.Sk, a.causal = L.causal;
     a.scale = L.scale, a.scale_log2 = L.scale * kLog2e;
     a.mods = L.mods;
+    a.grad_scale = L.mods.softcap > 0.f ? 4.f * L.mods.softcap * L.scale : L.scale;
     a.nlse = L.nlse, a.ndelta = L.ndelta, a.ext = static_cast<const uint4 *>(L.ext), a.pitch = pitch;
     const BwdSplit cut = bwd_split(L.B, L.Hq, L.Hkv, L.Sq, L.Sk, L.dk, L.causal);
     a.kv_len = cut.kv_len, a.kv_parts = cut.kv_parts, a.q_len = cut.q_len, a.q_parts = cut.q_parts;

@@ -47,7 +47,7 @@ static __device__ int g_prefill_err;
 struct PrefillArgs {
     int Hq, group, Sq, Sk;
     float scale, scale_log2;
-    ScoreMods mods;  // used by the MODS instantiation only
+    ScoreMods mods;  // unused by MODS_NONE
     int causal;
     char *o;
     int64_t o_sb, o_sh, o_ss;
@@ -94,7 +94,7 @@ enum { B_QFULL = 0, B_DRAIN = 1, B_SFULL = 2, B_PREADY = 4, B_PVDONE = 6, B_RING
 
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: rescale when the max grows by > 2^8
 
-template <int DK, int DV, int BN, int NST, bool MODS>
+template <int DK, int DV, int BN, int NST, ModsKind KIND>
 __global__ void __launch_bounds__(192, 1)
 prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                const __grid_constant__ CUtensorMap tmV, const PrefillArgs a) {
@@ -274,14 +274,14 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         // row max, so the exponent factor is 1.
         // Only a mask or a softcap changes the scores themselves; sinks act in
         // the epilogue alone.
-        const bool transform = MODS && (a.mods.mask != nullptr || a.mods.softcap != 0.f);
+        constexpr bool transform = KIND >= MODS_CAP;
         const float c = transform ? 1.f : a.scale_log2;
         // keys j < lim_all are visible to this row
         const int lim_all = qrow >= Sq ? 0 : (a.causal ? min(Sk, qrow + Sk - Sq + 1) : Sk);
-        const float slope = MODS ? alibi_slope(a.mods, hq) : 1.f;
-        const __half *mrow = MODS ? mask_row(a.mods, b, hq, qrow, a.Sq) : nullptr;
+        const float slope = KIND >= MODS_MASK ? alibi_slope(a.mods, hq) : 1.f;
+        const __half *mrow = KIND >= MODS_MASK ? mask_row(a.mods, b, hq, qrow, a.Sq) : nullptr;
         // mask values are read for keys below min(Sk, row length); later keys read as 0
-        const int mkeys = MODS && a.mods.mask ? (int)min((int64_t)Sk, (int64_t)a.mods.m_ss) : Sk;
+        const int mkeys = KIND >= MODS_MASK ? (int)min((int64_t)Sk, (int64_t)a.mods.m_ss) : Sk;
         (void)mkeys;
         (void)slope;
         (void)mrow;
@@ -308,8 +308,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                 for (int i = 0; i < BN; ++i) x[i] = __uint_as_float(r[i]);
             }
             const int lim = lim_all - t * BN;
-            if (transform) {
-                modify_scores<BN>(x, a.mods, a.scale, slope, mrow, t * BN, mkeys, lim);
+            if constexpr (transform) {
+                modify_scores<BN, KIND>(x, a.mods, a.scale, slope, mrow, t * BN, mkeys, lim);
             } else if (lim < BN) {
 #pragma unroll
                 for (int i = 0; i < BN; ++i)
@@ -363,7 +363,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                     s0 += p0;
                     s1 += p1;
                     pk[i] = pack_bf16x2(p0, p1);
-                    if constexpr (MODS) {
+                    if constexpr (KIND != MODS_NONE) {
                         r0 += __uint_as_float(pk[i] << 16);
                         r1 += __uint_as_float(pk[i] & 0xffff0000u);
                     }
@@ -387,7 +387,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         const bool store = qrow < a.Sq;
         float inv_l = l_run > 0.f ? 1.f / l_run : 0.f;
         float lse2 = l_run > 0.f ? m_run + __log2f(l_run) : -INFINITY;
-        if constexpr (MODS) {
+        if constexpr (KIND != MODS_NONE) {
             inv_l = l_o > 0.f ? 1.f / l_o : 0.f;
             if (a.mods.sinks) inv_l = sink_normalise(m_run, l_run, l_o, a.mods.sinks[hq], &lse2);
         }
@@ -436,10 +436,10 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     }
 }
 
-template <int DK, int DV, int BN, int NST, bool MODS>
+template <int DK, int DV, int BN, int NST, ModsKind KIND>
 static cudaError_t launch_cfg(const PrefillLaunch &L, cudaStream_t stream) {
     using C = PrefillCfg<DK, DV, BN, NST>;
-    auto kern = prefill_kernel<DK, DV, BN, NST, MODS>;
+    auto kern = prefill_kernel<DK, DV, BN, NST, KIND>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
     if (e != cudaSuccess) return e;
     PrefillArgs a;
@@ -467,14 +467,20 @@ static cudaError_t launch_cfg(const PrefillLaunch &L, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
+template <int DK, int DV, int BN, int NST>
+static cudaError_t launch_cfg(const PrefillLaunch &L, cudaStream_t stream) {
+    const bool cap = L.mods.softcap != 0.f;
+    if (L.mods.mask)
+        return cap ? launch_cfg<DK, DV, BN, NST, MODS_CAP_MASK>(L, stream) : launch_cfg<DK, DV, BN, NST, MODS_MASK>(L, stream);
+    if (cap) return launch_cfg<DK, DV, BN, NST, MODS_CAP>(L, stream);
+    return L.has_mods ? launch_cfg<DK, DV, BN, NST, MODS_SINKS>(L, stream) : launch_cfg<DK, DV, BN, NST, MODS_NONE>(L, stream);
+}
+
 cudaError_t launch_prefill(const PrefillLaunch &L, cudaStream_t stream) {
-#define FA_PREFILL_CFG(DK_, DV_, BN_, NST_) \
-    (L.has_mods ? launch_cfg<DK_, DV_, BN_, NST_, true>(L, stream) : launch_cfg<DK_, DV_, BN_, NST_, false>(L, stream))
-    if (L.dk == 256 && L.dv == 256) return FA_PREFILL_CFG(256, 256, 64, 2);
-    if (L.dk == 192 && L.dv == 128) return FA_PREFILL_CFG(192, 128, 128, 2);
-    if (L.dk == 192 && L.dv == 192) return FA_PREFILL_CFG(192, 192, 64, 3);
-    if (L.dk == 320 && L.dv == 256) return FA_PREFILL_CFG(320, 256, 64, 2);
-#undef FA_PREFILL_CFG
+    if (L.dk == 256 && L.dv == 256) return launch_cfg<256, 256, 64, 2>(L, stream);
+    if (L.dk == 192 && L.dv == 128) return launch_cfg<192, 128, 128, 2>(L, stream);
+    if (L.dk == 192 && L.dv == 192) return launch_cfg<192, 192, 64, 3>(L, stream);
+    if (L.dk == 320 && L.dv == 256) return launch_cfg<320, 256, 64, 2>(L, stream);
     return cudaErrorInvalidValue;
 }
 

@@ -72,15 +72,12 @@ FA_DEV void trace(int ev, int t, int sub, int uc) {
 struct Prefill2Args {
     int Hq, group, Sq, Sk, BH, n_qp, n_units;
     float scale, scale_log2;
-    ScoreMods mods;  // used by the MODS instantiation only
+    ScoreMods mods;  // unused by MODS_NONE
     int causal;
     char *o;
     int64_t o_sb, o_sh, o_ss;
     int o_bf16;
     float *lse;
-    // The mask arrives through TMA into each softmax group's staging tile,
-    // 64 keys at a time (MODS with a mask, two-tile kernel).
-    int mask_staged;
     // Paged K/V: block_table [B, max_blocks] and seq_lens [B] (NULL: dense).
     const int32_t *block_table;
     const int32_t *seq_lens;
@@ -230,7 +227,7 @@ FA_DEV bool p2_unit(const Prefill2Args &a, int round, UnitInfo &u) {
 constexpr int P2_THREADS = FA_P2_THREADS;
 constexpr int P2_SOFTMAX_WARP0 = P2_THREADS == 384 ? 4 : 2;
 
-template <int D, bool MODS>
+template <int D, ModsKind KIND>
 __global__ void __launch_bounds__(P2_THREADS, 1)
 prefill2_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
@@ -391,7 +388,7 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                     mbar_wait_drain(v_full(k % NSTV), (uint32_t)(k / NSTV) & 1u);
             }
         }
-    } else if (MODS && warp >= 2 && a.mask_staged) {
+    } else if (KIND >= MODS_MASK && warp >= 2) {
         // ----------------------------------------------- mask loaders --
         // Warp 2 + i fills query tile i's staging tile with 64-key chunks of
         // the mask (128 rows x 128 bytes, 128-byte swizzle; rows past Sq and
@@ -598,8 +595,7 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         // row max, so the exponent factor is 1.
         // Only a mask or a softcap changes the scores themselves; sinks act in
         // the epilogue alone.
-        const bool transform = MODS && (a.mods.mask != nullptr || a.mods.softcap != 0.f);
-        const float c = transform ? 1.f : a.scale_log2;
+        const float c = KIND >= MODS_CAP ? 1.f : a.scale_log2;
         int scnt = 0, pv_base = 0, uc = 0, mcnt = 0;
         bool ok = true;
         UnitInfo u;
@@ -610,10 +606,8 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             const int qrow = u.q0 + 128 * ti + row;
             const int lim_all =
                 qrow >= u.Sq ? 0 : (a.causal ? min(u.Sk, qrow + u.Sk - u.Sq + 1) : u.Sk);
-            const float slope = MODS ? alibi_slope(a.mods, u.hq) : 1.f;
-            const __half *mrow = MODS ? mask_row(a.mods, u.b, u.hq, qrow, a.Sq) : nullptr;
+            const float slope = KIND >= MODS_MASK ? alibi_slope(a.mods, u.hq) : 1.f;
             (void)slope;
-            (void)mrow;
             // l_run sums the fp32 weights (it gives the LSE).  With modifiers,
             // l_o sums the bf16-rounded weights the PV MMA actually uses and
             // normalises O, so that the few-key rows ALiBi and masks produce
@@ -640,7 +634,7 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 }
                 if (lane == 0) TRACE(11 + ti, t, qd);
                 const int lim = lim_all - t * BN;
-                if (MODS && a.mask_staged) {
+                if constexpr (KIND >= MODS_MASK) {
                     // this row's 64 mask values of each chunk from the staging tile
 #pragma unroll
                     for (int h = 0; h < BN / 64; ++h) {
@@ -650,12 +644,14 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                         for (int j = 0; j < 8; ++j) w[j] = *reinterpret_cast<const uint4 *>(mstg + ((j ^ (row & 7)) << 4));
                         mbar_arrive(bar(P2_MEMPTY + ti));
                         ++mcnt;
-                        modify_chunk(&x[64 * h], w, a.mods, a.scale, slope);
+                        modify_chunk<KIND, true>(&x[64 * h], w, a.mods, a.scale, slope);
                     }
                     if (!ok) break;
                     hide_keys<BN>(x, lim);
-                } else if (transform) {
-                    modify_scores<BN>(x, a.mods, a.scale, slope, mrow, t * BN, u.Sk, lim);
+                } else if constexpr (KIND == MODS_CAP) {
+#pragma unroll
+                    for (int k = 0; k < BN; k += 4) softcap4_joint(x + k, a.scale, a.mods.softcap);
+                    hide_keys<BN>(x, lim);
                 } else if (lim < BN) {
 #pragma unroll
                     for (int k = 0; k < BN; ++k)
@@ -749,7 +745,7 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                             else
                                 acc0 = f2_add(acc0, f2_pack(p0, p1));
                             pk[k] = pack_bf16x2(p0, p1);
-                            if constexpr (MODS)
+                            if constexpr (KIND != MODS_NONE)
                                 accr = f2_add(accr, f2_pack(__uint_as_float(pk[k] << 16),
                                                             __uint_as_float(pk[k] & 0xffff0000u)));
                         }
@@ -768,7 +764,7 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                     f2_unpack(acc0, u0, u1);
                     f2_unpack(acc1, u2, u3);
                     l_run += (u0 + u1) + (u2 + u3);
-                    if constexpr (MODS) {
+                    if constexpr (KIND != MODS_NONE) {
                         float r0, r1;
                         f2_unpack(accr, r0, r1);
                         l_o += r0 + r1;
@@ -831,7 +827,7 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             mbar_arrive(bar(P2_OFREE + ti));  // O of this tile may be overwritten by the next unit
             float inv_l = l_run > 0.f ? 1.f / l_run : 0.f;
             float lse2 = l_run > 0.f ? m_run + __log2f(l_run) : -INFINITY;
-            if constexpr (MODS) {
+            if constexpr (KIND != MODS_NONE) {
                 inv_l = l_o > 0.f ? 1.f / l_o : 0.f;
                 if (a.mods.sinks) inv_l = sink_normalise(m_run, l_run, l_o, a.mods.sinks[u.hq], &lse2);
             }
@@ -879,7 +875,7 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                     store_slice(ch, ch * 32, w);
                 }
             }
-            if (MODS && a.mask_staged && row == 0) {
+            if (KIND >= MODS_MASK && row == 0) {
                 bulk_wait_read0();  // the last O store has read the staging tile
                 mbar_arrive(bar(P2_SFREE + ti));
             }
@@ -896,10 +892,10 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     }
 }
 
-template <int D, bool MODS>
+template <int D, ModsKind KIND>
 static cudaError_t launch_p2(const PrefillLaunch &L, int num_sms, cudaStream_t stream) {
     using C = P2Cfg<D>;
-    auto kern = prefill2_kernel<D, MODS>;
+    auto kern = prefill2_kernel<D, KIND>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
     if (e != cudaSuccess) return e;
     Prefill2Args a;
@@ -920,7 +916,6 @@ static cudaError_t launch_p2(const PrefillLaunch &L, int num_sms, cudaStream_t s
     a.o_ss = L.o_ss;
     a.o_bf16 = L.o_bf16;
     a.lse = L.lse;
-    a.mask_staged = MODS && L.mask_staged ? 1 : 0;
     a.block_table = L.block_table;
     a.seq_lens = L.seq_lens;
     a.q_lens = L.q_lens;
@@ -940,11 +935,19 @@ static cudaError_t launch_p2(const PrefillLaunch &L, int num_sms, cudaStream_t s
     return cudaGetLastError();
 }
 
+template <int D>
+static cudaError_t launch_p2(const PrefillLaunch &L, int num_sms, cudaStream_t stream) {
+    if (L.mask_staged)
+        return L.mods.softcap != 0.f ? launch_p2<D, MODS_CAP_MASK>(L, num_sms, stream)
+                                     : launch_p2<D, MODS_MASK>(L, num_sms, stream);
+    if (L.mods.softcap != 0.f) return launch_p2<D, MODS_CAP>(L, num_sms, stream);
+    return L.has_mods ? launch_p2<D, MODS_SINKS>(L, num_sms, stream) : launch_p2<D, MODS_NONE>(L, num_sms, stream);
+}
+
 cudaError_t launch_prefill2(const PrefillLaunch &L, int num_sms, cudaStream_t stream) {
     switch (L.dk) {
-        case 64: return L.has_mods ? launch_p2<64, true>(L, num_sms, stream) : launch_p2<64, false>(L, num_sms, stream);
-        case 128:
-            return L.has_mods ? launch_p2<128, true>(L, num_sms, stream) : launch_p2<128, false>(L, num_sms, stream);
+        case 64: return launch_p2<64>(L, num_sms, stream);
+        case 128: return launch_p2<128>(L, num_sms, stream);
         default: return cudaErrorInvalidValue;
     }
 }
