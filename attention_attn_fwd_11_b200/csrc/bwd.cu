@@ -174,13 +174,9 @@ struct BwdItem {
 // longest walks first (key tile 0 sees the most queries, the last query tile
 // the most keys), so that what is taken last is short.
 template <bool KV, int BN>
-FA_DEV BwdItem bwd_item(const BwdArgs &a, int i) {
+FA_DEV BwdItem bwd_tile(const BwdArgs &a, int turn, int bh) {  // a whole walk
     BwdItem it;
     const int H = KV ? a.Hkv : a.Hq;
-    const unsigned per = (unsigned)(a.B * H), idx = (unsigned)(KV ? i : i - a.kv_items);
-    const int bh = (int)(idx % per), parts = KV ? a.kv_parts : a.q_parts, len = KV ? a.kv_len : a.q_len;
-    int turn = (int)(idx / per), part = 0;
-    if (len > 0) part = turn % parts, turn /= parts;
     const int xt = KV ? turn : (a.Sq + 127) / 128 - 1 - turn;
     it.b = bh / H;
     it.h = bh % H;
@@ -198,6 +194,15 @@ FA_DEV BwdItem bwd_item(const BwdArgs &a, int i) {
         it.whole = it.n_y;
     }
     it.n = it.whole, it.y = 0, it.h_first = KV ? it.h * (a.Hq / a.Hkv) : it.h;
+    return it;
+}
+template <bool KV, int BN>
+FA_DEV BwdItem bwd_item(const BwdArgs &a, int i) {
+    const unsigned per = (unsigned)(a.B * (KV ? a.Hkv : a.Hq)), idx = (unsigned)(KV ? i : i - a.kv_items);
+    const int parts = KV ? a.kv_parts : a.q_parts, len = KV ? a.kv_len : a.q_len;
+    int turn = (int)(idx / per), part = 0;
+    if (len > 0) part = turn % parts, turn /= parts;
+    BwdItem it = bwd_tile<KV, BN>(a, turn, (int)(idx % per));
     if (len > 0) {
         const int t0 = part * len;
         it.n = min(len, max(0, it.whole - t0));
@@ -910,9 +915,10 @@ __global__ void __launch_bounds__(512) bwd_join_kernel(const BwdArgs a, int kv_b
         const int tile = block / (ACC / 16), col = block % (ACC / 16) * 16;
         const unsigned per = (unsigned)(a.B * (KV ? a.Hkv : a.Hq));
         const int parts = KV ? a.kv_parts : a.q_parts, len = KV ? a.kv_len : a.q_len;
-        // the tile's first part; the others follow `per` items apart
+        // the tile's first part; the others follow `per` items apart (a tile
+        // that sees nothing has none, and gets zeros)
         const unsigned first = (unsigned)tile / per * (unsigned)parts * per + (unsigned)tile % per;
-        const BwdItem it = bwd_item<KV, BN>(a, (int)first + (KV ? 0 : a.kv_items));
+        const BwdItem it = bwd_tile<KV, BN>(a, (int)((unsigned)tile / per), (int)((unsigned)tile % per));
         const int n = (it.whole + len - 1) / len;
         const float4 *from = reinterpret_cast<const float4 *>(KV ? a.kv_part : a.q_part) + col / 4 * 128 + row;
         float4 s[4] = {};
@@ -1106,7 +1112,7 @@ cudaError_t launch_tiles(const BwdLaunch &L, const BwdArgs &a, int num_sms, cuda
     e = cudaLaunchKernelEx(&cfg, kern, L.tmQx, L.tmKx, L.tmVx, L.tmDOx, L.tmQy, L.tmKy, L.tmVy, L.tmDOy, a);
     if (e != cudaSuccess || a.kv_len + a.q_len == 0) return e;
     const int kv = a.kv_len ? a.kv_items / a.kv_parts * ((DK + DV) / 16) : 0;
-    const int q = a.q_len ? (a.items - a.kv_items) / a.q_parts * (DK / 16) : 0;
+    const int q = a.q_len ? a.B * a.Hq * ((a.Sq + 127) / 128) * (DK / 16) : 0;
     bwd_join_kernel<DK, DV><<<kv + q, 512, 0, stream>>>(a, kv);
     return cudaGetLastError();
 }
@@ -1137,10 +1143,12 @@ double bwd_makespan(double nk, double k, double nq, double q) {
 // 16 x 4096: 24.6 and 57; 1 head, 4096 x 4096, causal: 38.6 and 63.5; but 8
 // heads, 1024 x 1024, causal (walks of 8, a share of 3.5): 28.5 and 24.5, so
 // left whole.
-BwdSplit bwd_split(int B, int Hq, int Hkv, int Sq, int Sk, int dk, int causal) {
+BwdSplit bwd_split(int B, int Hq, int Hkv, int Sq, int Sk, int dk, int dv, int causal) {
     BwdSplit s = {0, 1, 0, 1, 0, 0};
     if (B <= 0 || Sq <= 0 || Sk <= 0) return s;
     const int64_t BN = bwd_walk(dk), nk = (int64_t)B * Hkv * ((Sk + 127) / 128), nq = (int64_t)B * Hq * ((Sq + 127) / 128);
+    const int64_t nq_live = causal && Sq > Sk ? nq - (int64_t)B * Hq * ((Sq - Sk) / 128) : nq;
+    const double room = fmax(256e6, 4.0 * B * ((double)Hq * Sq * dk + (double)Hkv * Sk * (dk + dv)));
     // The longest walks, and how long the mean one is beside it.
     const int64_t kv = Hq / Hkv * ((Sq + BN - 1) / BN - (causal && Sq > Sk ? (Sq - Sk) / BN : 0));
     const int64_t q = (Sk + BN - 1) / BN;
@@ -1154,15 +1162,16 @@ BwdSplit bwd_split(int B, int Hq, int Hkv, int Sq, int Sk, int dk, int causal) {
     for (int64_t len = 2; len < longest && (double)len < 2 * share + 8; len += len < 8 ? 1 : len / 4) {
         // parts of even length; under a causal mask the mean walk ends half a part early
         const int64_t pk = (kv + len - 1) / len, lk = (kv + pk - 1) / pk, pq = (q + len - 1) / len, lq = (q + pq - 1) / pq;
+        if (512 * ((pk > 1 ? (double)(nk * pk) * (dk + dv) : 0) + (pq > 1 ? (double)(nq_live * pq) * dk : 0)) > room) continue;
         const double ck = pk == 1 ? nk : ceil(causal ? kv_tiles / (double)lk + 0.5 * nk : (double)(nk * pk));
-        const double cq = pq == 1 ? nq : ceil(causal ? q_tiles / (double)lq + 0.5 * nq : (double)(nq * pq));
+        const double cq = pq == 1 ? nq : ceil(causal ? q_tiles / (double)lq + 0.5 * nq_live : (double)(nq * pq));
         if (kJoin + share + kItem * (ck + cq) / kSms >= best) continue;  // the even share alone
         const double t = kJoin + fmax((double)(lk > lq ? lk : lq) + kItem,
                                       bwd_makespan(ck, kv_tiles / ck + kItem, cq, q_tiles / cq + kItem));
         if (t >= best) continue;
         best = t;
         s.kv_len = pk == 1 ? 0 : (int)lk, s.kv_parts = (int)pk, s.kv_chunks = pk == 1 ? 0 : nk * pk;
-        s.q_len = pq == 1 ? 0 : (int)lq, s.q_parts = (int)pq, s.q_chunks = pq == 1 ? 0 : nq * pq;
+        s.q_len = pq == 1 ? 0 : (int)lq, s.q_parts = (int)pq, s.q_chunks = pq == 1 ? 0 : nq_live * pq;
     }
     return s;
 }
@@ -1196,11 +1205,11 @@ cudaError_t launch_bwd(const BwdLaunch &L, int num_sms, cudaStream_t stream) {
     a.mods = L.mods;
     a.grad_scale = L.mods.softcap > 0.f ? 4.f * L.mods.softcap * L.scale : L.scale;
     a.nlse = L.nlse, a.ndelta = L.ndelta, a.ext = static_cast<const uint4 *>(L.ext), a.pitch = pitch;
-    const BwdSplit cut = bwd_split(L.B, L.Hq, L.Hkv, L.Sq, L.Sk, L.dk, L.causal);
+    const BwdSplit cut = bwd_split(L.B, L.Hq, L.Hkv, L.Sq, L.Sk, L.dk, L.dv, L.causal);
     a.kv_len = cut.kv_len, a.kv_parts = cut.kv_parts, a.q_len = cut.q_len, a.q_parts = cut.q_parts;
     a.kv_part = L.part, a.q_part = L.part + cut.kv_chunks * 128 * (L.dk + L.dv);
     a.kv_items = L.B * L.Hkv * ((L.Sk + 127) / 128) * cut.kv_parts;
-    a.items = a.kv_items + L.B * L.Hq * ((L.Sq + 127) / 128) * cut.q_parts;
+    a.items = a.kv_items + (cut.q_len ? (int)cut.q_chunks : L.B * L.Hq * ((L.Sq + 127) / 128));
     a.next = L.next;
     a.gq = BwdGrad{static_cast<char *>(L.gq), L.gq_sb, L.gq_sh, L.gq_ss};
     a.gk = BwdGrad{static_cast<char *>(L.gk), L.gk_sb, L.gk_sh, L.gk_ss};

@@ -419,7 +419,7 @@ size_t bwd_row_bytes(const fa_bwd_params *p) {  // of the row LSE, of D, and a q
 // The rows' LSE and D, the tile counter, and the parts of walks that are cut.
 size_t bwd_bytes(const fa_bwd_params *p, bool causal) {
     return 6 * bwd_row_bytes(p) + 256 +
-           fa::bwd_split(p->B, p->Hq, p->Hkv, p->Sq, p->Sk, p->dk, causal).bytes(p->dk, p->dv);
+           fa::bwd_split(p->B, p->Hq, p->Hkv, p->Sq, p->Sk, p->dk, p->dv, causal).bytes(p->dk, p->dv);
 }
 
 // A gradient's strides: vector stores of 16 bytes, rows that do not overlap.
@@ -1131,6 +1131,14 @@ fa_status fa_bwd_workspace_size(const fa_bwd_params *p, size_t *bytes) {
     if (!bytes) return fail(FA_ERR_INVALID_ARG, "fa_bwd_workspace_size: bytes is NULL");
     const size_t full = bwd_bytes(p, false), causal = bwd_bytes(p, true);
     *bytes = full > causal ? full : causal;
+    return FA_OK;
+}
+
+fa_status fa_bwd_workspace_need(const fa_bwd_params *p, size_t *bytes) {
+    fa_status st = check_bwd(p);
+    if (st != FA_OK) return st;
+    if (!bytes) return fail(FA_ERR_INVALID_ARG, "fa_bwd_workspace_need: bytes is NULL");
+    *bytes = bwd_bytes(p, p->causal != 0);
     return FA_OK;
 }
 

@@ -231,7 +231,7 @@ struct BwdSplit {
         return 512 * ((size_t)kv_chunks * (size_t)(dk + dv) + (size_t)q_chunks * (size_t)dk);
     }
 };
-BwdSplit bwd_split(int B, int Hq, int Hkv, int Sq, int Sk, int dk, int causal);
+BwdSplit bwd_split(int B, int Hq, int Hkv, int Sq, int Sk, int dk, int dv, int causal);
 cudaError_t launch_bwd(const BwdLaunch &L, int num_sms, cudaStream_t stream);
 cudaError_t bwd_device_error(int clear, int *code);
 

@@ -173,6 +173,8 @@ def load():
         lib.fa_kv_dequant_n.restype = _i32
         lib.fa_bwd_workspace_size.argtypes = [ctypes.POINTER(BwdParams), ctypes.POINTER(ctypes.c_size_t)]
         lib.fa_bwd_workspace_size.restype = _i32
+        lib.fa_bwd_workspace_need.argtypes = [ctypes.POINTER(BwdParams), ctypes.POINTER(ctypes.c_size_t)]
+        lib.fa_bwd_workspace_need.restype = _i32
         lib.fa_bwd.argtypes = [ctypes.POINTER(BwdParams), _vp]
         lib.fa_bwd.restype = _i32
         lib.fa_rope.argtypes = [ctypes.POINTER(RopeParams), _vp]
@@ -346,9 +348,16 @@ def _bwd_sizes(q, k, v):
     return p
 
 
-def bwd_workspace_bytes(q, k, v):
+def bwd_workspace_bytes(q, k, v, causal=None):
+    """Workspace of bwd() for these shapes, causal or not, or (given causal)
+    for that alone.  A smaller shape can need more than a larger one."""
     n = ctypes.c_size_t(0)
-    _check(load().fa_bwd_workspace_size(ctypes.byref(_bwd_sizes(q, k, v)), ctypes.byref(n)))
+    p = _bwd_sizes(q, k, v)
+    if causal is None:
+        _check(load().fa_bwd_workspace_size(ctypes.byref(p), ctypes.byref(n)))
+    else:
+        p.causal = 1 if causal else 0
+        _check(load().fa_bwd_workspace_need(ctypes.byref(p), ctypes.byref(n)))
     return n.value
 
 
@@ -422,7 +431,7 @@ def bwd(q, k, v, o, lse, do, scale=None, causal=False, mask=None, max_bias=0.0, 
     ref = ctypes.byref(p)
     if workspace is None:
         n = ctypes.c_size_t(0)
-        _check(lib.fa_bwd_workspace_size(ref, ctypes.byref(n)))
+        _check(lib.fa_bwd_workspace_need(ref, ctypes.byref(n)))
         workspace = torch.empty(n.value, device=q.device, dtype=torch.uint8)
     p.workspace, p.workspace_bytes = _workspace(workspace)
     _check(lib.fa_bwd(ref, _stream()))

@@ -168,7 +168,7 @@ fa_status fa_fwd(const fa_fwd_params *p, void *stream);
  *     -sum over rows of exp(sink_h - lse) D.
  *   Rows with no visible key (lse -inf) get gq = 0 and add nothing.  There is
  *   no gradient of the mask.  Keys that no query sees get gk = gv = 0.
- *   workspace: at least fa_bwd_workspace_size() bytes, 256-byte aligned,
+ *   workspace: at least fa_bwd_workspace_need() bytes, 256-byte aligned,
  *     overwritten on every call.
  * Scores, P, D and every sum are fp32; P and dS are rounded once to bf16, the
  * operand type of the products that follow.  No sum is made with atomics:
@@ -205,8 +205,16 @@ typedef struct {
     size_t workspace_bytes;
 } fa_bwd_params;
 
-/* Workspace bytes for these shapes, causal or not; reads no pointer field. */
+/*
+ * Workspace bytes for these shapes, causal or not (size), or for p->causal
+ * alone (need); no pointer field is read.  24 bytes a query row, and where the
+ * work is cut into parts for more SMs their sums: at most the size of the
+ * gradients in fp32, or 256 MB.  Small work is cut, large is not, so a smaller
+ * shape can need MORE than a larger one (8 heads, 16 queries, 4096 keys: 5.4 MB
+ * for 2 batch entries, 0.3 MB for 4): ask for each shape.
+ */
 fa_status fa_bwd_workspace_size(const fa_bwd_params *p, size_t *bytes);
+fa_status fa_bwd_workspace_need(const fa_bwd_params *p, size_t *bytes);
 fa_status fa_bwd(const fa_bwd_params *p, void *stream);
 
 /*
