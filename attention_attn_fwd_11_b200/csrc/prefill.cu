@@ -385,10 +385,10 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                 have_o = false;
         }
         const bool store = qrow < a.Sq;
-        float inv_l = l_run > 0.f ? 1.f / l_run : 0.f;
-        float lse2 = l_run > 0.f ? m_run + __log2f(l_run) : -INFINITY;
+        float inv_l = l_run == 0.f ? 0.f : 1.f / l_run;  // (a NaN goes through)
+        float lse2 = l_run == 0.f ? -INFINITY : m_run + __log2f(l_run);
         if constexpr (KIND != MODS_NONE) {
-            inv_l = l_o > 0.f ? 1.f / l_o : 0.f;
+            inv_l = l_o == 0.f ? 0.f : 1.f / l_o;
             if (a.mods.sinks) inv_l = sink_normalise(m_run, l_run, l_o, a.mods.sinks[hq], &lse2);
         }
         const int64_t ooff = (int64_t)b * a.o_sb + (int64_t)hq * a.o_sh + (int64_t)qrow * a.o_ss;

@@ -825,10 +825,10 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             if (row == 0) TRACE(17 + ti, 0, 0);
             tc_fence_before();
             mbar_arrive(bar(P2_OFREE + ti));  // O of this tile may be overwritten by the next unit
-            float inv_l = l_run > 0.f ? 1.f / l_run : 0.f;
-            float lse2 = l_run > 0.f ? m_run + __log2f(l_run) : -INFINITY;
+            float inv_l = l_run == 0.f ? 0.f : 1.f / l_run;  // (a NaN goes through)
+            float lse2 = l_run == 0.f ? -INFINITY : m_run + __log2f(l_run);
             if constexpr (KIND != MODS_NONE) {
-                inv_l = l_o > 0.f ? 1.f / l_o : 0.f;
+                inv_l = l_o == 0.f ? 0.f : 1.f / l_o;
                 if (a.mods.sinks) inv_l = sink_normalise(m_run, l_run, l_o, a.mods.sinks[u.hq], &lse2);
             }
             if (qrow >= u.Sq) lse2 = -INFINITY;  // past the sequence's new rows: not a query (sinks aside)

@@ -108,8 +108,8 @@ enum {
  *   <= Hq, m0 = 2^(-max_bias/n), m1 = 2^(-max_bias/(2n)).  The slope scales
  *   the mask (which then holds position distances); without a mask it has
  *   no effect.
- * A score that is NaN stays NaN through each of these, and makes O NaN in
- *   the rows that see its key; keys hidden by the causal rule or past Sk may
+ * A score that is NaN stays NaN through each of these, and makes O and LSE
+ *   NaN in the rows that see its key; keys hidden by the causal rule or past Sk may
  *   hold anything.
  * sinks: NULL, or [Hq] fp32 logits (natural-log units): one more term
  *   exp(sink_h) in each row's softmax denominator, with no value row.  The
