@@ -1203,7 +1203,7 @@ cudaError_t launch_bwd(const BwdLaunch &L, int num_sms, cudaStream_t stream) {
     a.B = L.B, a.Hq = L.Hq, a.Hkv = L.Hkv, a.Sq = L.Sq, a.Sk = L.Sk, a.causal = L.causal;
     a.scale = L.scale, a.scale_log2 = L.scale * kLog2e;
     a.mods = L.mods;
-    a.grad_scale = L.mods.softcap > 0.f ? 4.f * L.mods.softcap * L.scale : L.scale;
+    a.grad_scale = L.mods.softcap > 0.f ? 4.f * (L.mods.softcap * L.scale) : L.scale;
     a.nlse = L.nlse, a.ndelta = L.ndelta, a.ext = static_cast<const uint4 *>(L.ext), a.pitch = pitch;
     const BwdSplit cut = bwd_split(L.B, L.Hq, L.Hkv, L.Sq, L.Sk, L.dk, L.dv, L.causal);
     a.kv_len = cut.kv_len, a.kv_parts = cut.kv_parts, a.q_len = cut.q_len, a.q_parts = cut.q_parts;

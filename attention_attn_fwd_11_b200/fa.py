@@ -375,6 +375,8 @@ def bwd(q, k, v, o, lse, do, scale=None, causal=False, mask=None, max_bias=0.0, 
                    grad_dtype, workspace)
     _need_current_device(q, k, v, o, lse, do, mask, sinks, dlse, dq, dk, dv, workspace)
     bf16 = torch.bfloat16
+    if lse is None:
+        raise ValueError("lse, the log-sum-exp that fwd() returns, must be given")
     if q.dtype != bf16 or k.dtype != bf16 or v.dtype != bf16 or do.dtype != bf16:
         raise ValueError("q, k, v and do must be bf16")
     qs, ks, vs, os = q.shape, k.shape, v.shape, o.shape

@@ -137,3 +137,20 @@ def test_the_outer_stream_is_current_again_after_a_refusal(world):
     with pytest.raises(ValueError):
         fa.rope(z(2, 3), None, stream=world.given)
     assert torch.cuda.current_stream() is world.outer
+
+
+@pytest.mark.parametrize("name", sorted(calls()))
+def test_every_argument_reaches_the_call_on_the_stream(monkeypatch, name):
+    seen = []
+    monkeypatch.setattr(fa, "_on", lambda stream, call, *args, **kwargs: seen.append((stream, call, args, kwargs)))
+    f = getattr(fa, name)
+    names = [n for n, p in inspect.signature(f).parameters.items() if p.kind is not p.VAR_KEYWORD]
+    given = {n: object() for n in names}
+    if name == "fwd_quant":
+        given["softcap"] = object()
+    f(**given)
+    (stream, call, args, kwargs), = seen
+    got = inspect.signature(call).bind(*args, **kwargs).arguments
+    got.update(got.pop("mods", {}))
+    assert stream is given.pop("stream") and call is f and got.pop("stream", None) is None
+    assert got == given
