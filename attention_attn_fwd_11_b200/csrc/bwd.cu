@@ -77,8 +77,7 @@ struct BwdGrad {  // an output [B, H, S, d]
 
 struct BwdArgs {
     int B, Hq, Hkv, Sq, Sk, causal;
-    float scale, scale_log2;
-    float grad_scale;  // of dQ and dK: the scale, times what softcap4_slope leaves out
+    float scale, scale_log2;  // of dQ and dK (with what softcap4_slope leaves out); of the scores
     ScoreMods mods;
     // -LSE and -D of every row.  The row kernel may still be writing them when
     // the tile kernel starts: read behind its griddepcontrol.wait, with plain
@@ -94,6 +93,7 @@ struct BwdArgs {
     BwdGrad gq, gk, gv;
     int g_bf16;
     float *gsinks;  // NULL: not asked for
+    float cap_scale;  // of the scores under a softcap
 };
 
 // (dS is ready on two barriers in turn: dQ's workers may finish a tile before
@@ -576,7 +576,7 @@ struct BwdWorker {
                     }
                     if constexpr (MODS) {
                         if constexpr (CAPPED) {
-                            softcap4_slope(v, cap, a.scale, a.mods.softcap);
+                            softcap4_slope(v, cap, a.cap_scale, a.mods.softcap);
                         } else {
 #pragma unroll
                             for (int j = 0; j < 4; ++j) v[j] *= a.scale_log2;
@@ -718,7 +718,7 @@ struct BwdWorker {
                 for (int i = 0; i < 32; ++i) r[i] = 0u;
             }
             store_rows(KV ? (second ? a.gv : a.gk) : a.gq, a.g_bf16, it.b, it.h, row0, S, second ? col - DK : col, r,
-                       second ? 1.f : a.grad_scale, lane);
+                       second ? 1.f : a.scale, lane);
         }
         return true;
     }
@@ -938,7 +938,7 @@ __global__ void __launch_bounds__(512) bwd_join_kernel(const BwdArgs a, int kv_b
         const int S = KV ? a.Sk : a.Sq;
         if (group > 0 || it.x0 + row >= S) return;
         const bool second = col >= DK;
-        const float f = second ? 1.f : a.grad_scale;
+        const float f = second ? 1.f : a.scale;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
 #pragma unroll
@@ -1201,9 +1201,9 @@ cudaError_t launch_bwd(const BwdLaunch &L, int num_sms, cudaStream_t stream) {
     }
     BwdArgs a = {};
     a.B = L.B, a.Hq = L.Hq, a.Hkv = L.Hkv, a.Sq = L.Sq, a.Sk = L.Sk, a.causal = L.causal;
-    a.scale = L.scale, a.scale_log2 = L.scale * kLog2e;
+    a.scale_log2 = L.scale * kLog2e, a.cap_scale = L.scale;
     a.mods = L.mods;
-    a.grad_scale = L.mods.softcap > 0.f ? 4.f * (L.mods.softcap * L.scale) : L.scale;
+    a.scale = L.mods.softcap > 0.f ? 4.f * (L.mods.softcap * L.scale) : L.scale;
     a.nlse = L.nlse, a.ndelta = L.ndelta, a.ext = static_cast<const uint4 *>(L.ext), a.pitch = pitch;
     const BwdSplit cut = bwd_split(L.B, L.Hq, L.Hkv, L.Sq, L.Sk, L.dk, L.dv, L.causal);
     a.kv_len = cut.kv_len, a.kv_parts = cut.kv_parts, a.q_len = cut.q_len, a.q_parts = cut.q_parts;
