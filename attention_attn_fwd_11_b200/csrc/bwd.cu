@@ -50,7 +50,7 @@
 //   causal, 2 x 16 heads x 2048 x 128:  124 us in bursts, 141 to 144 sustained (floor 52)
 //   causal, 32 on 8 heads x 4096 x 128: 436 and 455 (209)
 //   causal, 2 x 16 x 2048, 192 / 128:   175 and 184 to 190 (68)
-//   mask, ALiBi, softcap and sinks, 2 x 8 x 1024 x 128: 66 (13)
+//   mask, ALiBi, softcap and sinks, 2 x 8 x 1024 x 128: 66 to 67 (13)
 // The first spends 131 us in the tile kernel under a profiler, its tensor pipe
 // 51 % active, its exponentials' pipe 31 %.  Sustained, the power limit sets
 // the pace: fewer cycles (a second issuing warp, 4 %) bought a lower clock and
@@ -725,7 +725,8 @@ struct BwdWorker {
 };
 
 // ---- warp 2: the sinks' gradient, a head at a time ---------------------------
-// A double a lane, in the order of the rows, and then the lanes.
+// A double a lane, in the order of the rows, and then the lanes; each term is a
+// product in fp32, whose factors have no more bits.
 FA_DEV void sink_gradients(const BwdArgs &a, int lane) {
     for (int h = blockIdx.x; h < a.Hq; h += gridDim.x) {
         const float sk = __ldg(a.mods.sinks + h);

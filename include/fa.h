@@ -109,8 +109,8 @@ enum {
  *   the mask (which then holds position distances); without a mask it has
  *   no effect.
  * A score that is NaN stays NaN through each of these, and makes O and LSE
- *   NaN in the rows that see its key; keys hidden by the causal rule or past Sk may
- *   hold anything.
+ *   NaN in the rows that see its key.  K rows that a query does not see by the
+ *   causal rule may hold anything; V rows must be finite (0 * NaN is NaN).
  * sinks: NULL, or [Hq] fp32 logits (natural-log units): one more term
  *   exp(sink_h) in each row's softmax denominator, with no value row.  The
  *   returned LSE includes it; a row with no visible key then gets O = 0 and
