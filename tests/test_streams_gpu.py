@@ -89,3 +89,30 @@ def test_results_used_on_the_callers_stream_and_let_go(name):
     for a, b in zip(copies, want):
         assert torch.equal(a, b)
     assert all(bool((t == 90).all()) for t in others)
+
+
+def test_on_a_stream_that_a_capture_forks():
+    q, k, v, do = rand(1, 4, 200, 128), rand(1, 2, 200, 128, seed=1), rand(1, 2, 200, 128, seed=2), rand(1, 4, 200, 128, seed=3)
+    inv, _ = fa.rope_frequencies(128)
+    fork = torch.cuda.Stream()
+
+    def step(stream):
+        qr, kr = fa.rope(q, inv, k=k, **stream)
+        o, lse = fa.fwd(qr, kr, v, **stream)
+        return [o, lse, *fa.bwd(qr, kr, v, o, lse, do, **stream)]
+
+    want = step({})
+    step(dict(stream=fork))
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        fork.wait_stream(torch.cuda.current_stream())
+        got = step(dict(stream=fork))
+        torch.cuda.current_stream().wait_stream(fork)
+    for _ in range(3):
+        for t in got:
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
